@@ -33,7 +33,14 @@ EXPORTS = (
     "fa_fwd_kvcache_noalloc", "fa_fwd_kvcache_noalloc_scratch_bytes", "fa_debug_exp2_selftest",
     "fa_fwd_ex", "fa_bwd_ex", "fa_varlen_fwd_ex", "fa_varlen_bwd_ex",
     "fa_fwd_kvcache_ex", "fa_fwd_kvcache_ex_workspace_size", "fa_merge_lse",
+    "fa_fwd_mod", "fa_bwd_mod", "fa_varlen_fwd_mod", "fa_varlen_bwd_mod",
+    "fa_fwd_kvcache_mod", "fa_fwd_kvcache_mod_workspace_size", "fa_rotary", "fa_rotary_tables",
 )
+
+FA_ROTARY_PLAIN = 0
+FA_ROTARY_LINEAR = 1
+FA_ROTARY_BASE = 2
+FA_ROTARY_BY_PARTS = 3
 
 FA_KERNEL_FWD = 0
 FA_KERNEL_BWD = 1
@@ -46,6 +53,8 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
 _U64 = ctypes.c_ulonglong
+_I64 = ctypes.c_longlong
+_D = ctypes.c_double
 
 _SIGS = {
     "fa_fwd_workspace_size": (_Z, [_I] * 6),
@@ -76,6 +85,15 @@ _SIGS = {
     "fa_merge_lse": (_I, [_P, _P] + [_I] * 6 + [_P, _P, _I, _P]),
     "fa_fwd_kvcache_ex": (_I, [_P] * 6 + [_I] + [_P] * 2 + [_I] * 3 + [_P] * 2 + [_I] * 5 + [_F] + [_I] * 4
                           + [_P, _Z, _P]),
+    "fa_fwd_mod": (_I, [_P] * 5 + [_I] * 6 + [_F, _I, _I, _I, _F, _P, _I, _P, _Z, _P]),
+    "fa_bwd_mod": (_I, [_P] * 9 + [_I] * 6 + [_F, _I, _I, _I, _I, _F, _P, _I, _P, _Z, _P]),
+    "fa_varlen_fwd_mod": (_I, [_P] * 7 + [_I] * 8 + [_F, _I, _I, _I, _F, _P, _I, _P, _Z, _P]),
+    "fa_varlen_bwd_mod": (_I, [_P] * 11 + [_I] * 8 + [_F, _I, _I, _I, _I, _F, _P, _I, _P, _Z, _P]),
+    "fa_fwd_kvcache_mod_workspace_size": (_Z, [_I] * 9),
+    "fa_fwd_kvcache_mod": (_I, [_P] * 6 + [_I] + [_P] * 2 + [_I] * 3 + [_P] * 2 + [_I] * 5 + [_F] + [_I] * 4
+                           + [_F, _P, _I, _P, _P, _I, _I, _I] + [_P, _Z, _P]),
+    "fa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_I64] * 6 + [_I, _I, _P]),
+    "fa_rotary_tables": (_I, [_P, _P, _I, _I, _D, _I, _D, _I, _D, _D, _D, _P]),
 }
 
 _lib = None
@@ -227,6 +245,83 @@ def fa_fwd_kvcache_ex(q, k_cache, v_cache, cache_seqlens, k_new, v_new, seqlen_n
                                     _ptr(lse), B, Hq, Hkv, Sq, D, float(softmax_scale), int(bool(causal)),
                                     int(window_left), int(window_right), int(num_splits), _ptr(workspace),
                                     workspace_bytes, _stream(stream))
+
+
+def fa_fwd_mod(q, k, v, out, lse, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, window_left, window_right, softcap,
+               alibi_slopes, alibi_batch_stride, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().fa_fwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk, D,
+                             float(softmax_scale), int(bool(causal)), int(window_left), int(window_right),
+                             float(softcap), _ptr(alibi_slopes), int(alibi_batch_stride), _ptr(workspace),
+                             workspace_bytes, _stream(stream))
+
+
+def fa_bwd_mod(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, window_left,
+               window_right, deterministic, softcap, alibi_slopes, alibi_batch_stride, workspace, workspace_bytes,
+               stream=None) -> int:
+    return load().fa_bwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
+                             _ptr(dv), B, Hq, Hkv, Sq, Sk, D, float(softmax_scale), int(bool(causal)),
+                             int(window_left), int(window_right), int(bool(deterministic)), float(softcap),
+                             _ptr(alibi_slopes), int(alibi_batch_stride), _ptr(workspace), workspace_bytes,
+                             _stream(stream))
+
+
+def fa_varlen_fwd_mod(q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k, total_q,
+                      total_k, Hq, Hkv, D, softmax_scale, causal, window_left, window_right, softcap, alibi_slopes,
+                      alibi_batch_stride, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().fa_varlen_fwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
+                                    _ptr(cu_seqlens_k), num_seqs, max_seqlen_q, max_seqlen_k, total_q, total_k, Hq,
+                                    Hkv, D, float(softmax_scale), int(bool(causal)), int(window_left),
+                                    int(window_right), float(softcap), _ptr(alibi_slopes), int(alibi_batch_stride),
+                                    _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def fa_varlen_bwd_mod(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q,
+                      max_seqlen_k, total_q, total_k, Hq, Hkv, D, softmax_scale, causal, window_left, window_right,
+                      deterministic, softcap, alibi_slopes, alibi_batch_stride, workspace, workspace_bytes,
+                      stream=None) -> int:
+    return load().fa_varlen_bwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
+                                    _ptr(dv), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), num_seqs, max_seqlen_q,
+                                    max_seqlen_k, total_q, total_k, Hq, Hkv, D, float(softmax_scale),
+                                    int(bool(causal)), int(window_left), int(window_right), int(bool(deterministic)),
+                                    float(softcap), _ptr(alibi_slopes), int(alibi_batch_stride), _ptr(workspace),
+                                    workspace_bytes, _stream(stream))
+
+
+def fa_fwd_kvcache_mod_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits,
+                                      rotary_dim) -> int:
+    return load().fa_fwd_kvcache_mod_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits,
+                                                    rotary_dim)
+
+
+def fa_fwd_kvcache_mod(q, k_cache, v_cache, cache_seqlens, k_new, v_new, seqlen_new, cache_batch_idx, block_table,
+                       max_blocks_per_seq, cache_batch, cache_capacity, out, lse, B, Hq, Hkv, Sq, D, softmax_scale,
+                       causal, window_left, window_right, num_splits, softcap, alibi_slopes, alibi_batch_stride,
+                       rotary_cos, rotary_sin, rotary_len, rotary_dim, rotary_interleaved, workspace, workspace_bytes,
+                       stream=None) -> int:
+    return load().fa_fwd_kvcache_mod(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cache_seqlens), _ptr(k_new),
+                                     _ptr(v_new), int(seqlen_new), _ptr(cache_batch_idx), _ptr(block_table),
+                                     int(max_blocks_per_seq), int(cache_batch), int(cache_capacity), _ptr(out),
+                                     _ptr(lse), B, Hq, Hkv, Sq, D, float(softmax_scale), int(bool(causal)),
+                                     int(window_left), int(window_right), int(num_splits), float(softcap),
+                                     _ptr(alibi_slopes), int(alibi_batch_stride), _ptr(rotary_cos), _ptr(rotary_sin),
+                                     int(rotary_len), int(rotary_dim), int(bool(rotary_interleaved)), _ptr(workspace),
+                                     workspace_bytes, _stream(stream))
+
+
+def fa_rotary(x, y, rotary_cos, rotary_sin, cu_seqlens, seqlen_offsets, seqlen_offset, num_seqs, S, total, H, D,
+              rotary_dim, rotary_len, x_stride_seq, x_stride_tok, x_stride_head, y_stride_seq, y_stride_tok,
+              y_stride_head, interleaved, inverse, stream=None) -> int:
+    return load().fa_rotary(_ptr(x), _ptr(y), _ptr(rotary_cos), _ptr(rotary_sin), _ptr(cu_seqlens),
+                            _ptr(seqlen_offsets), int(seqlen_offset), num_seqs, S, total, H, D, rotary_dim, rotary_len,
+                            x_stride_seq, x_stride_tok, x_stride_head, y_stride_seq, y_stride_tok, y_stride_head,
+                            int(bool(interleaved)), int(bool(inverse)), _stream(stream))
+
+
+def fa_rotary_tables(rotary_cos, rotary_sin, rotary_len, rotary_dim, base, scaling, factor, original_len,
+                     low_rotations, high_rotations, amplitude, stream=None) -> int:
+    return load().fa_rotary_tables(_ptr(rotary_cos), _ptr(rotary_sin), rotary_len, rotary_dim, float(base),
+                                   int(scaling), float(factor), int(original_len), float(low_rotations),
+                                   float(high_rotations), float(amplitude), _stream(stream))
 
 
 def fa_merge_lse(o_parts, lse_parts, num_parts, B, S, H, D, parts_fp32, out, lse, out_fp32, stream=None) -> int:

@@ -117,6 +117,27 @@ static void window_sides(int causal, int window_left, int window_right, int* wl,
     if (causal) *wr = 0;
 }
 
+// Score modifiers: softcap = 0 (none) or positive with scale / softcap and softcap well inside fp32; slopes
+// NULL, or [Hq] (batch stride 0) or [B][Hq] floats (batch stride >= Hq).
+static int check_score(float scale, float softcap, const float* slopes, int slope_batch_stride, int Hq) {
+    if (!(softcap >= 0.f) || !isfinite(softcap)) return FA_ERR_INVALID_ARG;
+    if (softcap > 0.f) {
+        const float in = scale / softcap;
+        if (!(in >= 1e-20f && in <= 1e20f) || softcap > 1e20f) return FA_ERR_UNSUPPORTED;
+    }
+    if (slopes != nullptr) {
+        if (slope_batch_stride != 0 && slope_batch_stride < Hq) return FA_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(slopes) & 3u) return FA_ERR_ALIGNMENT;
+    }
+    return FA_OK;
+}
+
+static void set_score(Problem* pr, float softcap, const float* slopes, int slope_batch_stride) {
+    pr->softcap = softcap;
+    pr->slopes = slopes;
+    pr->slope_sB = slope_batch_stride;
+}
+
 static int check_tokens(long long tokens, int H, int D) {
     // element indices are formed in 64-bit, token coordinates of tile loads in int32
     if (tokens > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -205,6 +226,7 @@ static Problem dense_problem(const void* q, const void* k, const void* v, int B,
     pr.lse_sB = static_cast<long long>(Hq) * Sq;
     pr.lse_sH = Sq;
     pr.lse_sT = 0;
+    set_score(&pr, 0.f, nullptr, 0);
     return pr;
 }
 
@@ -217,8 +239,17 @@ int fa_fwd(const void* q, const void* k, const void* v, void* out, float* lse, i
 int fa_fwd_ex(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Hq, int Hkv, int Sq,
               int Sk, int D, float softmax_scale, int causal, int window_left, int window_right, void* workspace,
               size_t workspace_bytes, fa_stream_t stream) {
+    return fa_fwd_mod(q, k, v, out, lse, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, window_left, window_right, 0.f,
+                      nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Hq, int Hkv, int Sq,
+               int Sk, int D, float softmax_scale, int causal, int window_left, int window_right, float softcap,
+               const float* alibi_slopes, int alibi_batch_stride, void* workspace, size_t workspace_bytes,
+               fa_stream_t stream) {
     int st = validate_dense(q, k, v, B, Hq, Hkv, Sq, Sk, D, softmax_scale);
     if (st != FA_OK) return st;
+    if ((st = check_score(softmax_scale, softcap, alibi_slopes, alibi_batch_stride, Hq)) != FA_OK) return st;
     if (out == nullptr || lse == nullptr) return FA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(lse)) return FA_ERR_ALIGNMENT;
     int* counter = nullptr;
@@ -226,6 +257,7 @@ int fa_fwd_ex(const void* q, const void* k, const void* v, void* out, float* lse
     Device dev;
     if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
     Problem pr = dense_problem(q, k, v, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, window_left, window_right);
+    set_score(&pr, softcap, alibi_slopes, alibi_batch_stride);
     return launch_fwd(pr, out, lse, counter, dev, static_cast<cudaStream_t>(stream));
 }
 
@@ -248,8 +280,18 @@ int fa_bwd_ex(const void* q, const void* k, const void* v, const void* out, cons
               void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, float softmax_scale,
               int causal, int window_left, int window_right, int deterministic, void* workspace,
               size_t workspace_bytes, fa_stream_t stream) {
+    return fa_bwd_mod(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, window_left,
+                      window_right, deterministic, 0.f, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_bwd_mod(const void* q, const void* k, const void* v, const void* out, const void* dout, const float* lse,
+               void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, float softmax_scale,
+               int causal, int window_left, int window_right, int deterministic, float softcap,
+               const float* alibi_slopes, int alibi_batch_stride, void* workspace, size_t workspace_bytes,
+               fa_stream_t stream) {
     int st = validate_dense(q, k, v, B, Hq, Hkv, Sq, Sk, D, softmax_scale);
     if (st != FA_OK) return st;
+    if ((st = check_score(softmax_scale, softcap, alibi_slopes, alibi_batch_stride, Hq)) != FA_OK) return st;
     if (!out || !dout || !lse || !dq || !dk || !dv || !workspace) return FA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(dout) || !aligned16(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
         return FA_ERR_ALIGNMENT;
@@ -258,6 +300,7 @@ int fa_bwd_ex(const void* q, const void* k, const void* v, const void* out, cons
     Device dev;
     if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
     Problem pr = dense_problem(q, k, v, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, window_left, window_right);
+    set_score(&pr, softcap, alibi_slopes, alibi_batch_stride);
     return launch_bwd_timed(pr, out, dout, lse, dq, dk, dv, workspace, deterministic != 0, dev,
                             static_cast<cudaStream_t>(stream));
 }
@@ -300,6 +343,7 @@ static Problem varlen_problem(const void* q, const void* k, const void* v, const
     pr.lse_sB = 0;
     pr.lse_sH = total_q;
     pr.lse_sT = 1;
+    set_score(&pr, 0.f, nullptr, 0);
     return pr;
 }
 
@@ -318,9 +362,20 @@ int fa_varlen_fwd_ex(const void* q, const void* k, const void* v, void* out, flo
                      const int32_t* cu_seqlens_k, int num_seqs, int max_seqlen_q, int max_seqlen_k, int total_q,
                      int total_k, int Hq, int Hkv, int D, float softmax_scale, int causal, int window_left,
                      int window_right, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+    return fa_varlen_fwd_mod(q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k,
+                             total_q, total_k, Hq, Hkv, D, softmax_scale, causal, window_left, window_right, 0.f,
+                             nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_varlen_fwd_mod(const void* q, const void* k, const void* v, void* out, float* lse, const int32_t* cu_seqlens_q,
+                      const int32_t* cu_seqlens_k, int num_seqs, int max_seqlen_q, int max_seqlen_k, int total_q,
+                      int total_k, int Hq, int Hkv, int D, float softmax_scale, int causal, int window_left,
+                      int window_right, float softcap, const float* alibi_slopes, int alibi_batch_stride,
+                      void* workspace, size_t workspace_bytes, fa_stream_t stream) {
     int st = validate_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k, total_q, total_k,
                              Hq, Hkv, D, softmax_scale);
     if (st != FA_OK) return st;
+    if ((st = check_score(softmax_scale, softcap, alibi_slopes, alibi_batch_stride, Hq)) != FA_OK) return st;
     if (!out || !lse) return FA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(lse)) return FA_ERR_ALIGNMENT;
     int* counter = nullptr;
@@ -329,6 +384,7 @@ int fa_varlen_fwd_ex(const void* q, const void* k, const void* v, void* out, flo
     if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
     Problem pr = varlen_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k, total_q,
                                 total_k, Hq, Hkv, D, softmax_scale, causal, window_left, window_right);
+    set_score(&pr, softcap, alibi_slopes, alibi_batch_stride);
     return launch_fwd(pr, out, lse, counter, dev, static_cast<cudaStream_t>(stream));
 }
 
@@ -354,9 +410,21 @@ int fa_varlen_bwd_ex(const void* q, const void* k, const void* v, const void* ou
                      int num_seqs, int max_seqlen_q, int max_seqlen_k, int total_q, int total_k, int Hq, int Hkv,
                      int D, float softmax_scale, int causal, int window_left, int window_right, int deterministic,
                      void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+    return fa_varlen_bwd_mod(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q,
+                             max_seqlen_k, total_q, total_k, Hq, Hkv, D, softmax_scale, causal, window_left,
+                             window_right, deterministic, 0.f, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_varlen_bwd_mod(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                      const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_seqlens_q,
+                      const int32_t* cu_seqlens_k, int num_seqs, int max_seqlen_q, int max_seqlen_k, int total_q,
+                      int total_k, int Hq, int Hkv, int D, float softmax_scale, int causal, int window_left,
+                      int window_right, int deterministic, float softcap, const float* alibi_slopes,
+                      int alibi_batch_stride, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
     int st = validate_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k, total_q, total_k,
                              Hq, Hkv, D, softmax_scale);
     if (st != FA_OK) return st;
+    if ((st = check_score(softmax_scale, softcap, alibi_slopes, alibi_batch_stride, Hq)) != FA_OK) return st;
     if (!out || !dout || !lse || !dq || !dk || !dv || !workspace) return FA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(dout) || !aligned16(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
         return FA_ERR_ALIGNMENT;
@@ -366,6 +434,7 @@ int fa_varlen_bwd_ex(const void* q, const void* k, const void* v, const void* ou
     if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
     Problem pr = varlen_problem(q, k, v, cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k, total_q,
                                 total_k, Hq, Hkv, D, softmax_scale, causal, window_left, window_right);
+    set_score(&pr, softcap, alibi_slopes, alibi_batch_stride);
     return launch_bwd_timed(pr, out, dout, lse, dq, dk, dv, workspace, deterministic != 0, dev,
                             static_cast<cudaStream_t>(stream));
 }
@@ -424,8 +493,8 @@ int fa_fwd_kvcache(const void* q, const void* k_cache, const void* v_cache, cons
     return run_kv_call(c, workspace, workspace_bytes, stream);
 }
 
-size_t fa_fwd_kvcache_ex_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
-                                        int max_blocks_per_seq, int num_splits) {
+static size_t kv_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity, int max_blocks_per_seq,
+                                int num_splits, int rotary_dim) {
     KvCall c = plain_kv_call(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hq, Hkv, Sq, cache_capacity, D,
                              1.0f, 0, num_splits);
     if (max_blocks_per_seq < 0) return 0;
@@ -434,8 +503,14 @@ size_t fa_fwd_kvcache_ex_workspace_size(int B, int Hq, int Hkv, int Sq, int D, i
         c.block_table = &paged_tag;   // only its presence matters for the sizes
         c.max_blocks_per_seq = max_blocks_per_seq;
     }
+    c.rotary_dim = rotary_dim;
     if (kvcache_validate(c, false) != FA_OK) return 0;
     return kvcache_workspace_bytes(c, kvcache_chunk(c, 148));
+}
+
+size_t fa_fwd_kvcache_ex_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
+                                        int max_blocks_per_seq, int num_splits) {
+    return kv_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits, 0);
 }
 
 int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const int32_t* cache_seqlens, const void* k_new,
@@ -443,6 +518,27 @@ int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const int32_t
                       int max_blocks_per_seq, int cache_batch, int cache_capacity, void* out, float* lse, int B,
                       int Hq, int Hkv, int Sq, int D, float softmax_scale, int causal, int window_left,
                       int window_right, int num_splits, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+    return fa_fwd_kvcache_mod(q, k_cache, v_cache, cache_seqlens, k_new, v_new, seqlen_new, cache_batch_idx,
+                              block_table, max_blocks_per_seq, cache_batch, cache_capacity, out, lse, B, Hq, Hkv, Sq, D,
+                              softmax_scale, causal, window_left, window_right, num_splits, 0.f, nullptr, 0, nullptr,
+                              nullptr, 0, 0, 0, workspace, workspace_bytes, stream);
+}
+
+size_t fa_fwd_kvcache_mod_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
+                                         int max_blocks_per_seq, int num_splits, int rotary_dim) {
+    return kv_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits, rotary_dim);
+}
+
+int fa_fwd_kvcache_mod(const void* q, void* k_cache, void* v_cache, const int32_t* cache_seqlens, const void* k_new,
+                       const void* v_new, int seqlen_new, const int32_t* cache_batch_idx, const int32_t* block_table,
+                       int max_blocks_per_seq, int cache_batch, int cache_capacity, void* out, float* lse, int B,
+                       int Hq, int Hkv, int Sq, int D, float softmax_scale, int causal, int window_left,
+                       int window_right, int num_splits, float softcap, const float* alibi_slopes,
+                       int alibi_batch_stride, const float* rotary_cos, const float* rotary_sin, int rotary_len,
+                       int rotary_dim, int rotary_interleaved, void* workspace, size_t workspace_bytes,
+                       fa_stream_t stream) {
+    const int st = check_score(softmax_scale, softcap, alibi_slopes, alibi_batch_stride, Hq);
+    if (st != FA_OK) return st;
     KvCall c = plain_kv_call(q, k_cache, v_cache, cache_seqlens, out, lse, B, Hq, Hkv, Sq, cache_capacity, D,
                              softmax_scale, causal, num_splits);
     c.k_new = k_new;
@@ -454,7 +550,101 @@ int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const int32_t
     c.cache_batch = cache_batch;
     c.window_left = window_left;
     c.window_right = window_right;
+    c.softcap = softcap;
+    c.slopes = alibi_slopes;
+    c.slope_sB = alibi_batch_stride;
+    c.rotary_cos = rotary_cos;
+    c.rotary_sin = rotary_sin;
+    c.rotary_len = rotary_len;
+    c.rotary_dim = rotary_dim;
+    c.rotary_interleaved = rotary_interleaved;
     return run_kv_call(c, workspace, workspace_bytes, stream);
+}
+
+// ----------------------------------------------------------------------- rotary positions
+int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rotary_sin, const int32_t* cu_seqlens,
+              const int32_t* seqlen_offsets, int seqlen_offset, int num_seqs, int S, int total, int H, int D,
+              int rotary_dim, int rotary_len, long long x_stride_seq, long long x_stride_tok, long long x_stride_head,
+              long long y_stride_seq, long long y_stride_tok, long long y_stride_head, int interleaved, int inverse,
+              fa_stream_t stream) {
+    if (!x || !y || !rotary_cos || !rotary_sin) return FA_ERR_INVALID_ARG;
+    if (num_seqs <= 0 || H <= 0 || D <= 0 || rotary_len <= 0 || seqlen_offset < 0) return FA_ERR_INVALID_ARG;
+    if (cu_seqlens != nullptr ? total <= 0 : S <= 0) return FA_ERR_INVALID_ARG;
+    if (!supported_d(D)) return FA_ERR_UNSUPPORTED;
+    if (rotary_dim <= 0 || rotary_dim > D || rotary_dim % 16 != 0) return FA_ERR_INVALID_ARG;
+    if (rotary_len > kMaxSeqlen || S > kMaxSeqlen || seqlen_offset > kMaxSeqlen || num_seqs > kMaxSeqlen)
+        return FA_ERR_UNSUPPORTED;
+    RotaryCall c;
+    c.tokens = cu_seqlens != nullptr ? total : static_cast<long long>(num_seqs) * S;
+    const int st = check_tokens(c.tokens, H, D);
+    if (st != FA_OK) return st;
+    const long long xs[3] = {x_stride_seq, x_stride_tok, x_stride_head};
+    const long long ys[3] = {y_stride_seq, y_stride_tok, y_stride_head};
+    for (int i = 0; i < 3; ++i) {
+        // 16-byte pieces: strides in multiples of 8 values
+        if (xs[i] < 0 || ys[i] < 0) return FA_ERR_INVALID_ARG;
+        if (xs[i] % 8 != 0 || ys[i] % 8 != 0) return FA_ERR_ALIGNMENT;
+        c.x_stride[i] = xs[i];
+        c.y_stride[i] = ys[i];
+    }
+    // heads and tokens of y must not lie on each other (x may be broadcast)
+    const long long len = cu_seqlens != nullptr ? total : S;
+    if ((H > 1 && ys[2] < D) || (len > 1 && ys[1] < D) || (cu_seqlens == nullptr && num_seqs > 1 && ys[0] < D))
+        return FA_ERR_INVALID_ARG;
+    if (x == y && (xs[1] != ys[1] || xs[2] != ys[2] || (cu_seqlens == nullptr && xs[0] != ys[0])))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(rotary_cos) || !aligned16(rotary_sin)) return FA_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) || (reinterpret_cast<uintptr_t>(seqlen_offsets) & 3u))
+        return FA_ERR_ALIGNMENT;
+    Device dev;
+    if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
+    c.x = x;
+    c.y = y;
+    c.cos = rotary_cos;
+    c.sin = rotary_sin;
+    c.cu_seqlens = cu_seqlens;
+    c.offsets = seqlen_offsets;
+    c.offset = seqlen_offset;
+    c.num_seqs = num_seqs;
+    c.S = S;
+    c.H = H;
+    c.D = D;
+    c.rotary_dim = rotary_dim;
+    c.seqlen_ro = rotary_len;
+    c.interleaved = interleaved != 0;
+    c.inverse = inverse != 0;
+    return launch_rotary(c, dev, static_cast<cudaStream_t>(stream));
+}
+
+int fa_rotary_tables(float* rotary_cos, float* rotary_sin, int rotary_len, int rotary_dim, double base, int scaling,
+                     double factor, int original_len, double low_rotations, double high_rotations, double amplitude,
+                     fa_stream_t stream) {
+    if (!rotary_cos || !rotary_sin || rotary_len <= 0) return FA_ERR_INVALID_ARG;
+    if (rotary_dim <= 0 || rotary_dim % 16 != 0) return FA_ERR_INVALID_ARG;
+    if (rotary_dim > 256 || rotary_len > kMaxSeqlen) return FA_ERR_UNSUPPORTED;
+    if (!(base > 1.0) || !isfinite(base) || !isfinite(amplitude)) return FA_ERR_INVALID_ARG;
+    if (scaling < FA_ROTARY_PLAIN || scaling > FA_ROTARY_BY_PARTS) return FA_ERR_INVALID_ARG;
+    if (scaling != FA_ROTARY_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return FA_ERR_INVALID_ARG;
+    if (scaling == FA_ROTARY_BY_PARTS &&
+        (original_len <= 0 || !(low_rotations >= 0.0) || !(high_rotations > low_rotations) || !isfinite(high_rotations)))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(rotary_cos) || !aligned16(rotary_sin)) return FA_ERR_ALIGNMENT;
+    if (scaling == FA_ROTARY_BASE) base *= pow(factor, rotary_dim / (rotary_dim - 2.0));
+    double freq[128];
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double f = pow(base, -2.0 * i / rotary_dim);
+        if (scaling == FA_ROTARY_LINEAR) f /= factor;
+        if (scaling == FA_ROTARY_BY_PARTS) {
+            const double turns = original_len * f * 0.15915494309189533577;   // f / 2 pi per position
+            const double g = fmin(1.0, fmax(0.0, (turns - low_rotations) / (high_rotations - low_rotations)));
+            f = (1.0 - g) * f / factor + g * f;
+        }
+        freq[i] = f;
+    }
+    Device dev;
+    if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
+    return launch_rotary_table(rotary_cos, rotary_sin, rotary_len, rotary_dim, freq, static_cast<float>(amplitude),
+                               static_cast<cudaStream_t>(stream));
 }
 
 // ----------------------------------------------------------------------- diagnostics

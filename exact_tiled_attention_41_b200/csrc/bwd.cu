@@ -42,6 +42,7 @@
 // no reduce-adds, warps 8-11 idle) and computes dq in the query-tile-stationary
 // pass of bwd_dq.cu instead of steps 2's dQ and 3.
 #include "internal.h"
+#include "score.cuh"
 #include "sm100.cuh"
 
 #include <math.h>
@@ -85,6 +86,7 @@ struct BwdParams {
     int l2_keep;            // 1: reduce-adds into dQacc with the L2 evict_last policy
     unsigned long long timeout_ns;
     int* status;
+    ScoreParams sc;
 };
 
 struct BUnit {
@@ -173,7 +175,8 @@ struct BwdCfg {
     static_assert(2 * 128 * COMPUTE_REGS + 128 * DQ_REGS + 128 * OTHER_REGS <= THREADS * LAUNCH_REGS, "register split");
 };
 
-template <int D, bool DQ>
+// MODE: score modifiers (score.cuh)
+template <int D, bool DQ, int MODE>
 __global__ void __launch_bounds__(512, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(512, 1)
         const int gq = warp >> 2;                  // query columns [64 gq, 64 gq + 64)
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lb = tmem_lane_base(warp & 3);
-        const float c2 = p.scale_log2;
+        const float c2 = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;   // score (tanh) -> log2 units
         uint32_t unit_it = 0, q_it = 0, g_it = 0;
         bool ok = true;
         for (uint32_t fi = 0; ok; ++fi) {
@@ -496,6 +499,11 @@ __global__ void __launch_bounds__(512, 1)
                 const int qmin = q_lo - m0, qmax = q_hi - m0;
                 const bool full_row = qmin <= 64 * gq && qmax >= 64 * gq + 63;
                 const bool any_mask = __any_sync(0xffffffffu, !full_row);
+                float slope = 0.f, d0 = 0.f;   // distance of the warpgroup's first query column from the key
+                if constexpr ((MODE & kScoreBias) != 0) {
+                    slope = slope_log2(p.sc, t.b, t.hk * G + it / t.n_m);
+                    d0 = static_cast<float>(m0 + 64 * gq + (t.Lk - t.Lq) - kj);
+                }
                 const float* lse_t = sLSE + st * 128 + 64 * gq;
                 const float* del_t = sDel + st * 128 + 64 * gq;
                 const float2 c2v = make_float2(c2, c2);
@@ -506,7 +514,7 @@ __global__ void __launch_bounds__(512, 1)
                 // they share the exp2 unit; one pair in 6 measured best: +3 % dense, +6 % long-context
                 // GQA, +7 % varlen D = 64 over none, ahead of one in 3 or 4)
                 auto grad = [&](auto poly) {
-                constexpr int kEvery = decltype(poly)::value ? kBwdFmaExpEvery : 0;
+                constexpr int kEvery = decltype(poly)::value && !(MODE & kScoreCap) ? kBwdFmaExpEvery : 0;
                 constexpr int kMod = kEvery > 0 ? kEvery : 1;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -515,6 +523,7 @@ __global__ void __launch_bounds__(512, 1)
                     tmem_ld32(tmem + lb + C::COL_DP + 64 * gq + 32 * half, dh);
                     tmem_ld_wait_tie(sh);
                     reg_tie(dh);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc.in);
                     uint32_t pp[16], dd[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
@@ -526,7 +535,11 @@ __global__ void __launch_bounds__(512, 1)
                             const float dla = x == 0 ? d4.x : d4.z, dlb = x == 0 ? d4.y : d4.w;
                             const float2 sv = make_float2(__uint_as_float(sh[e + x]), __uint_as_float(sh[e + x + 1]));
                             const float2 dv = make_float2(__uint_as_float(dh[e + x]), __uint_as_float(dh[e + x + 1]));
-                            const float2 a = ffma2(sv, c2v, make_float2(la, lbv));
+                            float2 a = ffma2(sv, c2v, make_float2(la, lbv));
+                            if constexpr ((MODE & kScoreBias) != 0) {
+                                a.x += bias_log2(d0 + (half * 32 + e + x), slope);
+                                a.y += bias_log2(d0 + (half * 32 + e + x + 1), slope);
+                            }
                             float2 pr = (kEvery > 0 && ((e + x) / 2) % kMod == kMod - 1)
                                             ? exp2_fma2(a) : make_float2(ex2_approx(a.x), ex2_approx(a.y));
                             if (any_mask) {
@@ -534,7 +547,8 @@ __global__ void __launch_bounds__(512, 1)
                                 pr.x = (qc >= qmin && qc <= qmax) ? pr.x : 0.f;
                                 pr.y = (qc + 1 >= qmin && qc + 1 <= qmax) ? pr.y : 0.f;
                             }
-                            const float2 ds = fmul2(pr, fadd2(dv, make_float2(dla, dlb)));
+                            float2 ds = fmul2(pr, fadd2(dv, make_float2(dla, dlb)));
+                            if constexpr ((MODE & kScoreCap) != 0) ds = cap_gradient(ds, sv);
                             pp[(e + x) / 2] = pack_bf16x2(pr.x, pr.y);
                             dd[(e + x) / 2] = pack_bf16x2(ds.x, ds.y);
                         }
@@ -691,6 +705,7 @@ struct PPCfg {
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
+template <int MODE>
 __global__ void __launch_bounds__(384, 1)
     bwd_pp_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -880,7 +895,7 @@ __global__ void __launch_bounds__(384, 1)
         const int gb = warp >> 2;                  // buffer / item parity of this warpgroup
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lb = tmem_lane_base(warp & 3);
-        const float c2 = p.scale_log2;
+        const float c2 = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;   // score (tanh) -> log2 units
         const float2 c2v = make_float2(c2, c2);
         uint32_t unit_it = 0, q_it = 0, gi = 0;
         bool ok = true;
@@ -916,13 +931,18 @@ __global__ void __launch_bounds__(384, 1)
                     // allowed item query columns: qmin .. qmax
                     const int qmin = q_lo - row0, qmax = q_hi - row0;
                     const bool any_mask = __any_sync(0xffffffffu, !(qmin <= 0 && qmax >= 63));
+                    float slope = 0.f, d0 = 0.f;
+                    if constexpr ((MODE & kScoreBias) != 0) {
+                        slope = slope_log2(p.sc, t.b, t.hk * G + it / t.n_m);
+                        d0 = static_cast<float>(row0 + (t.Lk - t.Lq) - kj);
+                    }
                     const float* lse_t = sLSE + st * 64;
                     const float* del_t = sDel + st * 64;
                     // the same FMA-pipe share of the exponentials as bwd_kernel, on the same elements and under
                     // the same condition (no masked column in the warp's 64, the whole 128-row query tile inside
                     // the sequence), so both backward modes compute identical P^T and dS^T
                     auto grad = [&](auto poly) {
-                    constexpr int kEvery = decltype(poly)::value ? kBwdFmaExpEvery : 0;
+                    constexpr int kEvery = decltype(poly)::value && !(MODE & kScoreCap) ? kBwdFmaExpEvery : 0;
                     constexpr int kMod = kEvery > 0 ? kEvery : 1;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -931,6 +951,7 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_ld32(tmem + lb + C::COL_DP(gb) + 32 * half, dh);
                         tmem_ld_wait_tie(sh);
                         reg_tie(dh);
+                        if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc.in);
                         uint32_t pp[16], dd[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -942,7 +963,11 @@ __global__ void __launch_bounds__(384, 1)
                                 const float dla = x == 0 ? d4.x : d4.z, dlb = x == 0 ? d4.y : d4.w;
                                 const float2 sv = make_float2(__uint_as_float(sh[e + x]), __uint_as_float(sh[e + x + 1]));
                                 const float2 dv = make_float2(__uint_as_float(dh[e + x]), __uint_as_float(dh[e + x + 1]));
-                                const float2 a = ffma2(sv, c2v, make_float2(la, lbv));
+                                float2 a = ffma2(sv, c2v, make_float2(la, lbv));
+                                if constexpr ((MODE & kScoreBias) != 0) {
+                                    a.x += bias_log2(d0 + (half * 32 + e + x), slope);
+                                    a.y += bias_log2(d0 + (half * 32 + e + x + 1), slope);
+                                }
                                 float2 pr = (kEvery > 0 && ((e + x) / 2) % kMod == kMod - 1)
                                                 ? exp2_fma2(a) : make_float2(ex2_approx(a.x), ex2_approx(a.y));
                                 if (any_mask) {
@@ -950,7 +975,8 @@ __global__ void __launch_bounds__(384, 1)
                                     pr.x = (qc >= qmin && qc <= qmax) ? pr.x : 0.f;
                                     pr.y = (qc + 1 >= qmin && qc + 1 <= qmax) ? pr.y : 0.f;
                                 }
-                                const float2 ds = fmul2(pr, fadd2(dv, make_float2(dla, dlb)));
+                                float2 ds = fmul2(pr, fadd2(dv, make_float2(dla, dlb)));
+                                if constexpr ((MODE & kScoreCap) != 0) ds = cap_gradient(ds, sv);
                                 pp[(e + x) / 2] = pack_bf16x2(pr.x, pr.y);
                                 dd[(e + x) / 2] = pack_bf16x2(ds.x, ds.y);
                             }
@@ -1167,7 +1193,7 @@ int bwd_chunk_groups(int num_groups, int units_per_group, int group_q_heads, int
     return static_cast<int>((num_groups + n_chunks - 1) / n_chunks);
 }
 
-template <int D, bool DQ>
+template <int D, bool DQ, int MODE>
 static int run_bwd(const Problem& pr, const void* out, const void* dout, const float* lse, void* dq, void* dk, void* dv,
                    void* workspace, const Device& dev, cudaStream_t stream) {
     using C = BwdCfg<D>;
@@ -1229,8 +1255,9 @@ static int run_bwd(const Problem& pr, const void* out, const void* dout, const f
     p.counter = bwd_unit_counter(workspace, pr.Tq, pr.Hq, D);
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
+    p.sc = score_params(pr);
 
-    auto kern = bwd_kernel<D, DQ>;
+    auto kern = bwd_kernel<D, DQ, MODE>;
     static bool set[64] = {};
     if (!set[dev.id & 63]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM)) !=
@@ -1258,6 +1285,7 @@ static int run_bwd(const Problem& pr, const void* out, const void* dout, const f
 }
 
 // Head dim 128, deterministic: the two-items-in-flight main kernel, then the dQ pass.
+template <int MODE>
 static int run_bwd_pp(const Problem& pr, const void* out, const void* dout, const float* lse, void* dq, void* dk,
                       void* dv, void* workspace, const Device& dev, cudaStream_t stream) {
     using C = PPCfg;
@@ -1312,8 +1340,9 @@ static int run_bwd_pp(const Problem& pr, const void* out, const void* dout, cons
     p.counter = nullptr;
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
+    p.sc = score_params(pr);
 
-    auto kern = bwd_pp_kernel;
+    auto kern = bwd_pp_kernel<MODE>;
     static bool set[64] = {};
     if (!set[dev.id & 63]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM)) !=
@@ -1358,16 +1387,20 @@ static int run_bwd256(const Problem& pr, const void* out, const void* dout, cons
 
 int launch_bwd(const Problem& pr, const void* out, const void* dout, const float* lse, void* dq, void* dk, void* dv,
                void* workspace, bool deterministic, const Device& dev, cudaStream_t stream) {
-    switch (pr.D) {
-        case 64:
-            return deterministic ? run_bwd<64, false>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream)
-                                 : run_bwd<64, true>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream);
-        case 128:
-            return deterministic ? run_bwd_pp(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream)
-                                 : run_bwd<128, true>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream);
-        case 256: return run_bwd256(pr, out, dout, lse, dq, dk, dv, workspace, deterministic, dev, stream);
-        default: return 2;
-    }
+    if (pr.D == 256) return run_bwd256(pr, out, dout, lse, dq, dk, dv, workspace, deterministic, dev, stream);
+    auto run = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
+        switch (pr.D) {
+            case 64:
+                return deterministic ? run_bwd<64, false, MODE>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream)
+                                     : run_bwd<64, true, MODE>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream);
+            case 128:
+                return deterministic ? run_bwd_pp<MODE>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream)
+                                     : run_bwd<128, true, MODE>(pr, out, dout, lse, dq, dk, dv, workspace, dev, stream);
+            default: return 2;
+        }
+    };
+    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
 }
 
 }  // namespace fa

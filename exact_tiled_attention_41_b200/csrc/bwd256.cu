@@ -20,6 +20,7 @@
 // With DQ = false (the deterministic backward) dQ is left to the query-tile-stationary
 // pass of bwd_dq.cu: no dQ product, no reduce-adds, no convert.
 #include "internal.h"
+#include "score.cuh"
 #include "sm100.cuh"
 
 #include <math.h>
@@ -50,6 +51,7 @@ struct B256Params {
     int* counter;           // unit counter of the dynamic schedule (zeroed by the preprocess kernel)
     unsigned long long timeout_ns;
     int* status;
+    ScoreParams sc;
 };
 
 struct U256 {
@@ -139,7 +141,8 @@ struct Cfg {
 // and dV (the dO pairs).  Each releases the ring slots of its own pairs.  S^T of a tile overwrites the
 // packed P^T and dS^T of the previous tile (in the S^T columns), read by B's dV and A's own dK, so A waits
 // for B's previous dV there (dv_done).
-template <bool DQ>
+// MODE: score modifiers (score.cuh)
+template <bool DQ, int MODE>
 __global__ void __launch_bounds__(512, 1)
     bwd256_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(512, 1)
         const int gq = warp >> 2;                  // query columns [32 gq, 32 gq + 32)
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lb = tmem_lane_base(warp & 3);
-        const float c2 = p.scale_log2;
+        const float c2 = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;   // score (tanh) -> log2 units
         uint32_t unit_it = 0, q_it = 0;
         bool ok = true;
         for (uint32_t fi = 0; ok; ++fi) {
@@ -488,6 +491,12 @@ __global__ void __launch_bounds__(512, 1)
                 tmem_ld32(tmem + lb + C::COL_DP + 32 * gq, da);
                 tmem_ld_wait_tie(sa);
                 reg_tie(da);
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores(sa, p.sc.in);
+                float slope = 0.f, d0 = 0.f;   // distance of the warpgroup's first query column from the key
+                if constexpr ((MODE & kScoreBias) != 0) {
+                    slope = slope_log2(p.sc, t.b, t.hk * G + it / t.n_m);
+                    d0 = static_cast<float>(m0 + 32 * gq + (t.Lk - t.Lq) - kj);
+                }
                 const int qmin = q_lo - m0 - 32 * gq, qmax = q_hi - m0 - 32 * gq;
                 const bool any_mask = __any_sync(0xffffffffu, !(kvalid && qmin <= 0 && qmax >= 31));
                 const float2 c2v = make_float2(c2, c2);
@@ -496,13 +505,18 @@ __global__ void __launch_bounds__(512, 1)
                 for (int e = 0; e < 32; e += 2) {
                     const float2 sv = make_float2(__uint_as_float(sa[e]), __uint_as_float(sa[e + 1]));
                     const float2 dv = make_float2(__uint_as_float(da[e]), __uint_as_float(da[e + 1]));
-                    const float2 a = ffma2(sv, c2v, make_float2(nL[e], nL[e + 1]));
+                    float2 a = ffma2(sv, c2v, make_float2(nL[e], nL[e + 1]));
+                    if constexpr ((MODE & kScoreBias) != 0) {
+                        a.x += bias_log2(d0 + e, slope);
+                        a.y += bias_log2(d0 + (e + 1), slope);
+                    }
                     float2 pr = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                     if (any_mask) {
                         pr.x = (kvalid && e >= qmin && e <= qmax) ? pr.x : 0.f;
                         pr.y = (kvalid && e + 1 >= qmin && e + 1 <= qmax) ? pr.y : 0.f;
                     }
-                    const float2 ds = fmul2(pr, fadd2(dv, make_float2(nD[e], nD[e + 1])));
+                    float2 ds = fmul2(pr, fadd2(dv, make_float2(nD[e], nD[e + 1])));
+                    if constexpr ((MODE & kScoreCap) != 0) ds = cap_gradient(ds, sv);
                     pp[e / 2] = pack_bf16x2(pr.x, pr.y);
                     dd[e / 2] = pack_bf16x2(ds.x, ds.y);
                 }
@@ -581,7 +595,7 @@ __global__ void __launch_bounds__(256) bwd256_convert_kernel(const float* dq_acc
 
 }  // namespace
 
-template <bool DQ>
+template <bool DQ, int MODE>
 static int run_bwd256(const Problem& pr, const void* dout, const float* lse2, const float* delta, float* dq_acc,
                       void* dq, void* dk, void* dv, const Device& dev, cudaStream_t stream) {
     using C = Cfg;
@@ -619,7 +633,8 @@ static int run_bwd256(const Problem& pr, const void* dout, const float* lse2, co
     p.counter = bwd_unit_counter(dq_acc, pr.Tq, pr.Hq, D);   // dq_acc is the start of the workspace
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
-    auto kern = bwd256_kernel<DQ>;
+    p.sc = score_params(pr);
+    auto kern = bwd256_kernel<DQ, MODE>;
     static bool set[64] = {};
     if (!set[dev.id & 63]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM)) !=
@@ -647,8 +662,12 @@ static int run_bwd256(const Problem& pr, const void* dout, const float* lse2, co
 
 int launch_bwd256_main(const Problem& pr, const void* dout, const float* lse2, const float* delta, float* dq_acc,
                        void* dq, void* dk, void* dv, bool with_dq, const Device& dev, cudaStream_t stream) {
-    return with_dq ? run_bwd256<true>(pr, dout, lse2, delta, dq_acc, dq, dk, dv, dev, stream)
-                   : run_bwd256<false>(pr, dout, lse2, delta, dq_acc, dq, dk, dv, dev, stream);
+    auto run = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
+        return with_dq ? run_bwd256<true, MODE>(pr, dout, lse2, delta, dq_acc, dq, dk, dv, dev, stream)
+                       : run_bwd256<false, MODE>(pr, dout, lse2, delta, dq_acc, dq, dk, dv, dev, stream);
+    };
+    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
 }
 
 }  // namespace fa

@@ -29,6 +29,7 @@
 //   warps 10-11 idle.
 //   tensor memory: S0 [0,BK) | S1 [BK,2BK) | dP [2BK,3BK) | dQ [3BK,3BK+D)
 #include "internal.h"
+#include "score.cuh"
 #include "sm100.cuh"
 
 #include <math.h>
@@ -47,6 +48,7 @@ struct DqParams {
     int wl, wr;             // window sides, -1 = unbounded; a causal mask is wr = 0
     unsigned long long timeout_ns;
     int* status;
+    ScoreParams sc;
 };
 
 struct DqUnit {
@@ -116,7 +118,8 @@ struct DqCfg {
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-template <int D, int BK, int KST, int VST>
+// MODE: score modifiers (score.cuh)
+template <int D, int BK, int KST, int VST, int MODE>
 __global__ void __launch_bounds__(384, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(384, 1)
         const int wq = warp & 3;
         const int r = wq * 32 + lane;
         const uint32_t lb = tmem_lane_base(wq);
-        const float c2 = p.scale_log2;
+        const float c2 = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;   // score (tanh) -> log2 units
         const float2 c2v = make_float2(c2, c2);
         uint32_t gt = 0, unit_it = 0;
         bool ok = true;
@@ -320,6 +323,8 @@ __global__ void __launch_bounds__(384, 1)
             const float nl = valid ? -__ldg(p.lse2 + si) : -INFINITY;   // rows past the sequence: P = 0
             const float nd = valid ? -__ldg(p.delta + si) : 0.f;
             const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+            float slope = 0.f;
+            if constexpr ((MODE & kScoreBias) != 0) slope = slope_log2(p.sc, t.b, t.h);
             int key_lo = 0, key_hi = t.Lk - 1;
             if (p.wl >= 0) key_lo = max(0, row + (t.Lk - t.Lq) - p.wl);
             if (p.wr >= 0) key_hi = min(key_hi, row + (t.Lk - t.Lq) + p.wr);
@@ -340,15 +345,23 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_arrive(dp_free);
                 const int kbase = (t.kv0 + j) * BK + gw * HALF;   // key index of this thread's first column
                 const bool any_mask = __any_sync(0xffffffffu, kbase + HALF - 1 > key_hi || kbase < key_lo);
+                float d0 = 0.f;   // distance of the first column's key from the query
+                if constexpr ((MODE & kScoreBias) != 0) d0 = static_cast<float>(row + (t.Lk - t.Lq) - kbase);
 #pragma unroll
                 for (int cc = 0; cc < HALF / 32; ++cc) {
                     uint32_t sv[32];
                     tmem_ld32(tS + cc * 32, sv);
                     tmem_ld_wait_tie(sv);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sv, p.sc.in);
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float2 x = ffma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2v, nl2);
+                        const float2 sc = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                        float2 x = ffma2(sc, c2v, nl2);
+                        if constexpr ((MODE & kScoreBias) != 0) {
+                            x.x += bias_log2(d0 - (cc * 32 + e), slope);
+                            x.y += bias_log2(d0 - (cc * 32 + e + 1), slope);
+                        }
                         float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                         if (any_mask) {
                             const int kj = kbase + cc * 32 + e;
@@ -356,7 +369,8 @@ __global__ void __launch_bounds__(384, 1)
                             pr.y = (kj + 1 >= key_lo && kj + 1 <= key_hi) ? pr.y : 0.f;
                         }
                         const float2 dv = fadd2(make_float2(__uint_as_float(dp[cc][e]), __uint_as_float(dp[cc][e + 1])), nd2);
-                        const float2 ds = fmul2(pr, dv);
+                        float2 ds = fmul2(pr, dv);
+                        if constexpr ((MODE & kScoreCap) != 0) ds = cap_gradient(ds, sc);
                         pk[e / 2] = pack_bf16x2(ds.x, ds.y);
                     }
                     // packed columns [16 cc, 16 cc + 16) of the half: S columns already read
@@ -424,7 +438,7 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-template <int D, int BK, int KST, int VST>
+template <int D, int BK, int KST, int VST, int MODE>
 static int run_dq(const Problem& pr, const void* dout, const float* lse2, const float* delta, void* dq,
                   const Device& dev, cudaStream_t stream) {
     using C = DqCfg<D, BK, KST, VST>;
@@ -459,9 +473,10 @@ static int run_dq(const Problem& pr, const void* dout, const float* lse2, const 
     p.wr = pr.wr;
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
+    p.sc = score_params(pr);
     if (p.num_units == 0) return 0;
 
-    auto kern = dq_kernel<D, BK, KST, VST>;
+    auto kern = dq_kernel<D, BK, KST, VST, MODE>;
     static bool attr_set[64] = {};
     if (!attr_set[dev.id & 63]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM)) !=
@@ -478,12 +493,16 @@ static int run_dq(const Problem& pr, const void* dout, const float* lse2, const 
 
 int launch_bwd_dq(const Problem& pr, const void* dout, const float* lse2, const float* delta, void* dq,
                   const Device& dev, cudaStream_t stream) {
-    switch (pr.D) {
-        case 64: return run_dq<64, 128, 3, 3>(pr, dout, lse2, delta, dq, dev, stream);
-        case 128: return run_dq<128, 128, 2, 2>(pr, dout, lse2, delta, dq, dev, stream);
-        case 256: return run_dq<256, 64, 2, 1>(pr, dout, lse2, delta, dq, dev, stream);
-        default: return 2;
-    }
+    auto run = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
+        switch (pr.D) {
+            case 64: return run_dq<64, 128, 3, 3, MODE>(pr, dout, lse2, delta, dq, dev, stream);
+            case 128: return run_dq<128, 128, 2, 2, MODE>(pr, dout, lse2, delta, dq, dev, stream);
+            case 256: return run_dq<256, 64, 2, 1, MODE>(pr, dout, lse2, delta, dq, dev, stream);
+            default: return 2;
+        }
+    };
+    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
 }
 
 }  // namespace fa

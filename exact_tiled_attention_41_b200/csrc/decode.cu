@@ -29,6 +29,8 @@
 // tests fill it with NaN) cannot reach the result.
 #include "../../include/fa.h"
 #include "internal.h"
+#include "rotary.cuh"
+#include "score.cuh"
 #include "sm100.cuh"
 
 #include <math.h>
@@ -53,6 +55,14 @@ struct DecodeParams {
     float scale_log2;
     unsigned long long timeout_ns;
     int* status;
+    ScoreParams sc;
+};
+
+// Rotary tables of a call: rows x rd / 2 cosines and sines.
+struct RotaryTables {
+    const float* cos;
+    const float* sin;
+    int rows, rd, interleaved;
 };
 
 constexpr int kDecTile = 64;       // keys per pipeline stage
@@ -111,7 +121,9 @@ __device__ __forceinline__ uint32_t sw128(int row, int chunk) {
 template <int D>
 constexpr int dec_min_blocks() { return D == 256 ? 1 : 2; }
 
-template <int D>
+// MODE: score modifiers (score.cuh).  A tile's 16 x 64 scores cost the multi-function unit at most three
+// results each (tanh and exponential), under a fifth of the time its keys and values take to arrive.
+template <int D, int MODE>
 __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ DecodeParams p) {
@@ -202,7 +214,7 @@ __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
     }
 
     // ---------------------------------------------------------------- consumers
-    const float c2 = p.scale_log2;
+    const float c2 = (MODE & kScoreBias) ? 1.f : (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
     const int qr = lane >> 2;          // fragment rows qr and qr + 8 of the block
     const int qc = (lane & 3) * 2;     // fragment column pair
     const int ra = r0 + qr, rbr = r0 + qr + 8;
@@ -210,6 +222,13 @@ __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
     auto row_lo = [&](int r) { return p.wl >= 0 ? max(0, r / p.G + off - p.wl) : 0; };
     auto row_hi = [&](int r) { return p.wr >= 0 ? min(L - 1, r / p.G + off + p.wr) : L - 1; };
     const int lo_a = row_lo(ra), hi_a = row_hi(ra), lo_b = row_lo(rbr), hi_b = row_hi(rbr);
+    // slope and position of the two rows, for the distance bias
+    float sl_a = 0.f, sl_b = 0.f;
+    if constexpr ((MODE & kScoreBias) != 0) {
+        sl_a = slope_log2(p.sc, b, hk * p.G + ra % p.G);
+        sl_b = slope_log2(p.sc, b, hk * p.G + rbr % p.G);
+    }
+    const int at_a = ra / p.G + off, at_b = rbr / p.G + off;
     // Q as the A operand: row r is query head hk * G + r % G of token r / G; rows past R are zero
     uint32_t qa[KSTEPS][4];
     {
@@ -255,6 +274,20 @@ __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
                 mma_bf16_16816(sc[0], qa[kk], b0, b1);
                 mma_bf16_16816(sc[1], qa[kk], b2, b3);
             }
+        }
+        // ---- cap and bias
+        if constexpr ((MODE & kScoreCap) != 0) {
+            cap_scores(sc[0], p.sc.in);
+            cap_scores(sc[1], p.sc.in);
+        }
+        if constexpr ((MODE & kScoreBias) != 0) {
+            const float mul = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
+            const float da = static_cast<float>(at_a - kt - qc), db = static_cast<float>(at_b - kt - qc);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sc[t][e] = fmaf(sc[t][e], mul, bias_log2((e < 2 ? da : db) - (8 * t + (e & 1)), e < 2 ? sl_a : sl_b));
         }
         // ---- mask keys outside each row's range (which includes keys >= L)
         if (kt + 15 > hi_all || kt < lo_all) {
@@ -420,6 +453,30 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_consta
         lse[(static_cast<size_t>(b) * p.Hq + hq) * p.Sq + s] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
 }
 
+// Keys of sequence b before this call: cache_seqlens[b] kept inside what a sequence can hold.
+__device__ __forceinline__ int cached_keys(const DecodeParams& p, int b) {
+    return min(max(__ldg(p.seqlens + b), 0), p.kmax);
+}
+
+// Physical cache row of a new key at logical row `pos` of sequence b; -1 if it is not to be written: past
+// what the sequence can hold, or its batch index (reported by the split kernel) or block id (reported
+// here) is outside the cache.
+__device__ __forceinline__ long long append_row(const DecodeParams& p, int b, int pos, int lane) {
+    int bc = b;
+    if (p.page == 0 && p.batch_idx != nullptr) bc = __ldg(p.batch_idx + b);
+    if (p.page == 0 && (bc < 0 || bc >= p.cache_batch)) return -1;
+    if (pos >= p.kmax) return -1;
+    if (p.page > 0) {
+        const int blk = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + pos / p.page);
+        if (blk < 0 || blk >= p.cache_batch) {
+            if (lane == 0) atomicCAS(p.status, 0, FA_ERR_INVALID_ARG);
+            return -1;
+        }
+        return static_cast<long long>(blk) * p.page + pos % p.page;
+    }
+    return static_cast<long long>(bc) * p.kmax + pos;
+}
+
 // One warp per (batch row, new token, KV head): write k_new / v_new into the cache at logical row
 // cache_seqlens[b] + token.  Rows past what a sequence can hold are not written (and not attended).
 template <int D>
@@ -434,22 +491,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     const int hk = static_cast<int>(gw % p.Hkv);
     const int s = static_cast<int>((gw / p.Hkv) % Sn);
     const int b = static_cast<int>(gw / (static_cast<long long>(p.Hkv) * Sn));
-    int bc = b;
-    if (p.page == 0 && p.batch_idx != nullptr) bc = __ldg(p.batch_idx + b);
-    if (p.page == 0 && (bc < 0 || bc >= p.cache_batch)) return;   // reported by the split kernel
-    const int pos = max(__ldg(p.seqlens + b), 0) + s;
-    if (pos >= p.kmax) return;
-    int phys;
-    if (p.page > 0) {
-        const int blk = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + pos / p.page);
-        if (blk < 0 || blk >= p.cache_batch) {
-            if (lane == 0) atomicCAS(p.status, 0, FA_ERR_INVALID_ARG);
-            return;
-        }
-        phys = blk * p.page + pos % p.page;
-    } else {
-        phys = bc * p.kmax + pos;
-    }
+    const long long phys = append_row(p, b, cached_keys(p, b) + s, lane);
+    if (phys < 0) return;
     constexpr int V4 = D / 8;   // 16-byte pieces per row
     if (lane < V4) {
         const size_t src = ((static_cast<size_t>(b) * Sn + s) * p.Hkv + hk) * D;
@@ -457,6 +500,75 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         reinterpret_cast<uint4*>(k_cache + dst)[lane] = reinterpret_cast<const uint4*>(k_new + src)[lane];
         reinterpret_cast<uint4*>(v_cache + dst)[lane] = reinterpret_cast<const uint4*>(v_new + src)[lane];
     }
+}
+
+// The append with rotary positions: one warp per row of q (rotated into q_rot, which the split kernel then
+// reads) and per new (token, KV head) of the cache (k rotated on its way in, v copied).  New keys stand at
+// cache_seqlens[b] + token; query token i at cache_seqlens[b] + i under a causal mask or window, else at
+// cache_seqlens[b].  A lane takes one 16-byte piece and, for halves, reads its partner piece too.  A
+// position past the tables records an error, and the row becomes zeros.
+template <int D>
+__global__ void __launch_bounds__(256) kv_rotary_kernel(const __grid_constant__ DecodeParams p,
+                                                        const __nv_bfloat16* q, __nv_bfloat16* q_rot,
+                                                        __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
+                                                        const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
+                                                        const __grid_constant__ RotaryTables rt, int B, int Sn) {
+    grid_dep_launch();   // the split kernel may be scheduled; it waits for this grid before reading
+    const long long gw = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    const long long q_rows = static_cast<long long>(B) * p.Sq * p.Hq;
+    const __nv_bfloat16 *src, *vsrc = nullptr;
+    __nv_bfloat16 *dst, *vdst = nullptr;
+    int pos;
+    if (gw < q_rows) {
+        const int s = static_cast<int>((gw / p.Hq) % p.Sq), b = static_cast<int>(gw / p.Hq / p.Sq);
+        pos = cached_keys(p, b) + ((p.wl >= 0 || p.wr >= 0) ? s : 0);
+        src = q + gw * D;
+        dst = q_rot + gw * D;
+    } else {
+        const long long kw = gw - q_rows;
+        if (kw >= static_cast<long long>(B) * Sn * p.Hkv) return;
+        const int hk = static_cast<int>(kw % p.Hkv);
+        const int s = static_cast<int>((kw / p.Hkv) % Sn);
+        const int b = static_cast<int>(kw / p.Hkv / Sn);
+        pos = cached_keys(p, b) + s;
+        const long long row = append_row(p, b, pos, lane);
+        if (row < 0) return;
+        src = k_new + kw * D;
+        vsrc = v_new + kw * D;
+        dst = k_cache + (row * p.Hkv + hk) * D;
+        vdst = v_cache + (row * p.Hkv + hk) * D;
+    }
+    const bool bad = pos >= rt.rows;
+    if (bad && lane == 0) atomicCAS(p.status, 0, FA_ERR_INVALID_ARG);
+    const int d = lane * 8;
+    if (d >= D) return;
+    uint4 x = *reinterpret_cast<const uint4*>(src + d);
+    if (vsrc != nullptr) *reinterpret_cast<uint4*>(vdst + d) = *reinterpret_cast<const uint4*>(vsrc + d);
+    const int half = rt.rd / 2;
+    if (bad) {
+        x = make_uint4(0, 0, 0, 0);
+    } else if (d < rt.rd) {
+        const float* cr = rt.cos + static_cast<size_t>(pos) * half;
+        const float* sr = rt.sin + static_cast<size_t>(pos) * half;
+        if (rt.interleaved) {
+            x = rot_interleaved(x, __ldg(reinterpret_cast<const float4*>(cr + d / 2)),
+                                __ldg(reinterpret_cast<const float4*>(sr + d / 2)));
+        } else {
+            const bool low = d < half;
+            const int i = low ? d : d - half;
+            float c[8], s[8];
+            load8(cr + i, c);
+            load8(sr + i, s);
+            uint4 y = *reinterpret_cast<const uint4*>(src + (low ? d + half : d - half));
+            if (low) {
+                rot_halves(x, y, c, s);
+            } else {
+                rot_halves(y, x, c, s);
+            }
+        }
+    }
+    *reinterpret_cast<uint4*>(dst + d) = x;
 }
 
 // ------------------------------------------------------------------------------------------ host side
@@ -479,6 +591,14 @@ int kvcache_validate(const KvCall& c, bool pointers) {
         if ((c.seqlen_new > 0) != (c.k_new != nullptr)) return FA_ERR_INVALID_ARG;
     }
     if (c.seqlen_new < 0) return FA_ERR_INVALID_ARG;
+    if (c.rotary_dim != 0) {
+        // README: rotary applies to q and the new keys, and rotary_dim is a multiple of 16
+        if (c.rotary_dim < 0 || c.rotary_dim > c.D || c.rotary_dim % 16 != 0) return FA_ERR_INVALID_ARG;
+        if (pointers && (!c.rotary_cos || !c.rotary_sin || c.rotary_len <= 0 || c.seqlen_new == 0))
+            return FA_ERR_INVALID_ARG;
+    } else if (c.rotary_cos != nullptr || c.rotary_sin != nullptr) {
+        return FA_ERR_INVALID_ARG;
+    }
     if (c.block_table != nullptr) {
         // README: page_block_size must be a multiple of 256
         if (c.cache_capacity % 256 != 0 || c.max_blocks_per_seq <= 0) return FA_ERR_INVALID_ARG;
@@ -496,6 +616,8 @@ int kvcache_validate(const KvCall& c, bool pointers) {
     auto a16 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; };
     auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };
     if (!a16(c.q) || !a16(c.k_cache) || !a16(c.v_cache) || !a16(c.out)) return FA_ERR_ALIGNMENT;
+    if ((c.rotary_cos && !a16(c.rotary_cos)) || (c.rotary_sin && !a16(c.rotary_sin)) || (c.slopes && !a4(c.slopes)))
+        return FA_ERR_ALIGNMENT;
     if ((c.lse && !a16(c.lse)) || (c.k_new && (!a16(c.k_new) || !a16(c.v_new)))) return FA_ERR_ALIGNMENT;
     if (!a4(c.cache_seqlens) || (c.block_table && !a4(c.block_table)) || (c.cache_batch_idx && !a4(c.cache_batch_idx)))
         return FA_ERR_ALIGNMENT;
@@ -526,10 +648,13 @@ int kvcache_chunk(const KvCall& c, int num_sms) {
 size_t kvcache_workspace_bytes(const KvCall& c, int chunk) {
     const size_t max_chunks = (static_cast<size_t>(kvcache_chunk_limit(c)) + chunk - 1) / chunk;
     const size_t rows = static_cast<size_t>(c.B) * c.Hkv * max_chunks * rows_per_kv_head(c);
-    return ((rows * c.D * 4 + 255) & ~size_t(255)) + rows * 4;
+    const size_t partials = ((rows * c.D * 4 + 255) & ~size_t(255)) + rows * 4;
+    if (c.rotary_dim == 0) return partials;
+    // the rotated queries behind the partials
+    return ((partials + 255) & ~size_t(255)) + static_cast<size_t>(c.B) * c.Sq * c.Hq * c.D * 2;
 }
 
-template <int D>
+template <int D, int MODE>
 static int run_decode(const KvCall& c, int chunk, void* workspace, const Device& dev, cudaStream_t stream) {
     const int kmax = kvcache_chunk_limit(c);
     DecodeParams p;
@@ -557,11 +682,25 @@ static int run_decode(const KvCall& c, int chunk, void* workspace, const Device&
     p.scale_log2 = c.scale * 1.4426950408889634f;
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
+    p.sc = score_params(c.scale, c.softcap, c.slopes, c.slope_sB);
     const size_t rows = static_cast<size_t>(c.B) * c.Hkv * p.max_chunks * p.R;
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((rows * D * 4 + 255) & ~size_t(255)));
 
-    if (c.seqlen_new > 0) {
+    if (c.rotary_dim > 0) {
+        __nv_bfloat16* q_rot = reinterpret_cast<__nv_bfloat16*>(
+            static_cast<char*>(workspace) + (kvcache_workspace_bytes(c, chunk) - static_cast<size_t>(c.B) * c.Sq * c.Hq * D * 2));
+        const long long warps = static_cast<long long>(c.B) * (static_cast<long long>(c.Sq) * c.Hq +
+                                                               static_cast<long long>(c.seqlen_new) * c.Hkv);
+        const long long blocks = (warps + 7) / 8;
+        if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+        const RotaryTables rt = {c.rotary_cos, c.rotary_sin, c.rotary_len, c.rotary_dim, c.rotary_interleaved};
+        kv_rotary_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+            p, p.q, q_rot, static_cast<__nv_bfloat16*>(c.k_cache), static_cast<__nv_bfloat16*>(c.v_cache),
+            static_cast<const __nv_bfloat16*>(c.k_new), static_cast<const __nv_bfloat16*>(c.v_new), rt, c.B, c.seqlen_new);
+        if (cudaPeekAtLastError() != cudaSuccess) return FA_ERR_CUDA;
+        p.q = q_rot;
+    } else if (c.seqlen_new > 0) {
         const long long warps = static_cast<long long>(c.B) * c.seqlen_new * c.Hkv;
         const long long blocks = (warps + 7) / 8;
         if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -582,7 +721,7 @@ static int run_decode(const KvCall& c, int chunk, void* workspace, const Device&
     static_assert(merge_bytes <= kDecStages * stage_bytes, "merge buffer reuses the stage memory");
     const size_t smem = 1024 + kDecStages * stage_bytes + 2 * kDecStages * 8 + 16;
     static bool set[64] = {};
-    auto kern = decode_split_kernel<D>;
+    auto kern = decode_split_kernel<D, MODE>;
     if (!set[dev.id & 63]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
             cudaSuccess)
@@ -602,12 +741,16 @@ static int run_decode(const KvCall& c, int chunk, void* workspace, const Device&
 }
 
 int kvcache_launch(const KvCall& c, int chunk, void* workspace, const Device& dev, cudaStream_t stream) {
-    switch (c.D) {
-        case 64: return run_decode<64>(c, chunk, workspace, dev, stream);
-        case 128: return run_decode<128>(c, chunk, workspace, dev, stream);
-        case 256: return run_decode<256>(c, chunk, workspace, dev, stream);
-        default: return FA_ERR_UNSUPPORTED;
-    }
+    auto run = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
+        switch (c.D) {
+            case 64: return run_decode<64, MODE>(c, chunk, workspace, dev, stream);
+            case 128: return run_decode<128, MODE>(c, chunk, workspace, dev, stream);
+            case 256: return run_decode<256, MODE>(c, chunk, workspace, dev, stream);
+            default: return static_cast<int>(FA_ERR_UNSUPPORTED);
+        }
+    };
+    return with_score_mode(score_mode(c.softcap, c.slopes), run);
 }
 
 }  // namespace fa

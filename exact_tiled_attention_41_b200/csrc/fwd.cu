@@ -39,6 +39,7 @@
 // bf16/fp32 range).  With kDeferLog2 = 0 the reference follows every increase
 // of the running max.
 #include "internal.h"
+#include "score.cuh"
 #include "sm100.cuh"
 
 #include <math.h>
@@ -62,6 +63,7 @@ struct FwdParams {
     int* counter;   // unit counter of the dynamic schedule (zeroed before the launch), or NULL: static
     unsigned long long timeout_ns;
     int* status;
+    ScoreParams sc;
 };
 
 struct Unit {
@@ -78,7 +80,7 @@ struct Unit {
 // Unit u: the list is cut into chunks of p.chunk (sequence, query head) groups; inside a chunk the units
 // run query block by query block, the blocks that see the most keys first, over the chunk's groups (so
 // the CTAs of one moment share a few heads' K and V in L2).  p.chunk = all groups: heaviest first.
-template <int ROWS, int BK, bool LOCAL>
+template <int ROWS, int BK, bool LOCAL, bool REV>
 __device__ __forceinline__ Unit decode_unit(const FwdParams& p, int u) {
     Unit t;
     const int groups = p.num_seqs * p.Hq;
@@ -137,7 +139,7 @@ __device__ __forceinline__ Unit decode_unit(const FwdParams& p, int u) {
             // keys reachable from rows row_begin .. row_end-1 (lengths <= 2^30 and window sides < 2^30
             // keep every term inside int32)
             const int off = t.Lk - t.Lq;
-            const int lo = max(0, row_begin + off - p.wl);
+            const int lo = (REV && p.wl < 0) ? 0 : max(0, row_begin + off - p.wl);   // REV: any mask
             int hi = t.Lk - 1;
             if (p.wr >= 0) hi = min(hi, row_end - 1 + off + p.wr);
             if (hi >= lo) {
@@ -152,8 +154,8 @@ __device__ __forceinline__ Unit decode_unit(const FwdParams& p, int u) {
     t.n_kv = kmax > 0 ? kmax - kmin : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        t.lo[i] = e[i] > 0 ? f[i] - t.kv0 : 0;
-        t.hi[i] = e[i] > 0 ? e[i] - t.kv0 : 0;
+        t.lo[i] = e[i] > 0 ? (REV ? kmax - e[i] : f[i] - t.kv0) : 0;
+        t.hi[i] = e[i] > 0 ? (REV ? kmax - f[i] : e[i] - t.kv0) : 0;
     }
     return t;
 }
@@ -164,10 +166,13 @@ __device__ __forceinline__ int unit_lo(const Unit& t, int i) {
     else return 0;
 }
 __device__ __forceinline__ int unit_hi(const Unit& t, int i) { return i == 0 ? t.hi[0] : t.hi[1]; }
-template <bool LOCAL>
-__device__ __forceinline__ int unit_kv0(const Unit& t) {
-    if constexpr (LOCAL) return t.kv0;
-    else return 0;
+// KV tile of the sequence that the unit visits as its j-th.  REV: last tile first (decode_unit has then
+// turned lo[] and hi[] round too).
+template <bool LOCAL, bool REV>
+__device__ __forceinline__ int unit_tile(const Unit& t, int j) {
+    if constexpr (REV) return t.kv0 + t.n_kv - 1 - j;
+    else if constexpr (LOCAL) return t.kv0 + j;
+    else return j;
 }
 
 template <int D, int NQ, int BK, int KST>
@@ -215,13 +220,19 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // DYN: units come from p.counter through the shared-memory feed (varlen batches, head chunks sized for
 // L2); otherwise each role walks the static boustrophedon deal itself (dense problems whose K and V fit
 // L2: the static deal is balanced there, and the feed's per-unit hand-off measured 2-3 % slower).
-template <int D, int NQ, int BK, int KST, bool LOCAL, bool DYN>
+// MODE: score modifiers (score.cuh).  With any, KV tiles are visited last tile first: under a causal mask
+// and a distance bias the nearest keys then set the row's reference maximum at once, where the other
+// order raises it (and rescales O) at nearly every tile of a steep head.  One order for all modifiers keeps
+// the instances few; they use the LOCAL tile ranges whatever the mask.
+template <int D, int NQ, int BK, int KST, bool LOCAL, bool DYN, int MODE>
 __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D, NQ, BK, KST>;
     constexpr int BM = C::BM;
     constexpr int ROWS = BM * NQ;
+    constexpr bool REV = MODE != kScorePlain;
+    static_assert(LOCAL || !REV, "the turned tile ranges need lo[]");
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 u_next = take();
                 if (!publish(fi + 1, u_next)) break;
                 if (u >= p.num_units) continue;
-                const Unit t = decode_unit<ROWS, BK, LOCAL>(p, u);
+                const Unit t = decode_unit<ROWS, BK, LOCAL, REV>(p, u);
                 if (t.skip || t.n_kv == 0) continue;
                 const int hk = t.h / p.group;
                 for (int i = 0; i < NQ && ok; ++i) {
@@ -335,13 +346,13 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < C::NCHUNK; ++c)
                         tma_load_3d(smem_u32(sK + st * C::KV_BYTES + c * BK * 128), &tmK, k_full(st), c * 64, hk,
-                                    t.k_start + (unit_kv0<LOCAL>(t) + j) * BK);
+                                    t.k_start + unit_tile<LOCAL, REV>(t, j) * BK);
                     if (n > 0 && !mbar_wait(v_empty(st), (n - 1) & 1, w)) { ok = false; break; }
                     mbar_arrive_expect_tx(v_full(st), C::KV_BYTES);
 #pragma unroll
                     for (int c = 0; c < C::NCHUNK; ++c)
                         tma_load_3d(smem_u32(sV + st * C::KV_BYTES + c * BK * 128), &tmV, v_full(st), c * 64, hk,
-                                    t.k_start + (unit_kv0<LOCAL>(t) + j) * BK);
+                                    t.k_start + unit_tile<LOCAL, REV>(t, j) * BK);
                 }
                 if (!ok) break;
             }
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 }
                 if (u < 0) break;
                 if (u >= p.num_units) continue;
-                const Unit t = decode_unit<ROWS, BK, LOCAL>(p, u);
+                const Unit t = decode_unit<ROWS, BK, LOCAL, REV>(p, u);
                 if (t.skip || t.n_kv == 0) continue;
                 for (int i = 0; i < NQ && ok; ++i)
                     if (!mbar_wait(q_full(i), q_it & 1, w)) ok = false;
@@ -452,7 +463,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
         const uint32_t lane_base = tmem_lane_base(wq);
         const uint32_t tS = tmem + lane_base + C::S_COL(i);
         const uint32_t tO = tmem + lane_base + C::O_COL(i);
-        const float c2 = p.scale_log2;
+        // scores enter the exponentials as s * c2: with a bias s is already in log2 units, with a cap alone
+        // s is the tanh
+        const float c2 = (MODE & kScoreBias) ? 1.f : (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
         uint32_t s_it = 0, pv_total = 0;
         bool ok = true;
         for (uint32_t fi = 0; ok; ++fi) {
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             }
             if (u < 0) break;
             if (u >= p.num_units) continue;
-            const Unit t = decode_unit<ROWS, BK, LOCAL>(p, u);
+            const Unit t = decode_unit<ROWS, BK, LOCAL, REV>(p, u);
             if (t.skip) continue;
             const int row = t.q0 + i * BM + r;
             const bool valid = row < t.Lq;
@@ -482,8 +495,10 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             }
             // keys key_lo .. key_hi of the sequence are allowed for this row
             int key_lo = 0, key_hi = t.Lk - 1;
-            if (LOCAL) key_lo = max(0, row + (t.Lk - t.Lq) - p.wl);
+            if (LOCAL && (!REV || p.wl >= 0)) key_lo = max(0, row + (t.Lk - t.Lq) - p.wl);
             if (p.wr >= 0) key_hi = min(key_hi, row + (t.Lk - t.Lq) + p.wr);
+            float slope = 0.f;
+            if constexpr ((MODE & kScoreBias) != 0) slope = slope_log2(p.sc, t.b, t.h);
             float m_ref = -INFINITY;
             float l = 0.f;
             for (int j = 0; j < n_mine; ++j) {
@@ -501,7 +516,14 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
 #pragma unroll
                     for (int cc = 1; cc < BK / 32; ++cc) reg_tie(*reinterpret_cast<uint32_t(*)[32]>(sr + cc * 32));
                 }
-                const int kbase = (unit_kv0<LOCAL>(t) + lo_i + j) * BK;
+                const int kbase = unit_tile<LOCAL, REV>(t, lo_i + j) * BK;
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc.in);
+                if constexpr ((MODE & kScoreBias) != 0) {
+                    const float mul = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
+                    const float d0 = static_cast<float>(row + (t.Lk - t.Lq) - kbase);   // distance of column 0
+#pragma unroll
+                    for (int c = 0; c < BK; ++c) s[c] = fmaf(s[c], mul, bias_log2(d0 - c, slope));
+                }
                 const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
                 if (masked) {
 #pragma unroll
@@ -635,7 +657,7 @@ static int fwd_chunk_groups(const Problem& pr, int D, int m_blocks, int num_sms)
     return static_cast<int>((groups + n_chunks - 1) / n_chunks);
 }
 
-template <int D, int NQ, int BK, int KST, bool LOCAL, bool DYN>
+template <int D, int NQ, int BK, int KST, bool LOCAL, bool DYN, int MODE>
 static int run_fwd(const Problem& pr, void* out, float* lse, int* counter, const Device& dev, cudaStream_t stream) {
     using C = FwdCfg<D, NQ, BK, KST>;
     alignas(64) CUtensorMap mq, mk, mv;
@@ -673,10 +695,11 @@ static int run_fwd(const Problem& pr, void* out, float* lse, int* counter, const
     p.chunk = DYN ? fwd_chunk_groups(pr, D, p.m_blocks, dev.num_sms) : pr.num_seqs * pr.Hq;
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
+    p.sc = score_params(pr);
     if (p.num_units == 0) return 0;
     if (DYN && cudaMemsetAsync(counter, 0, sizeof(int), stream) != cudaSuccess) return 5;
 
-    auto kern = fwd_kernel<D, NQ, BK, KST, LOCAL, DYN>;
+    auto kern = fwd_kernel<D, NQ, BK, KST, LOCAL, DYN, MODE>;
     static bool attr_set[64] = {};
     if (!attr_set[dev.id & 63]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM)) !=
@@ -706,10 +729,19 @@ static int run_fwd_d(const Problem& pr, void* out, float* lse, int* counter, con
     const bool dyn = counter != nullptr &&
                      (pr.cu_q != nullptr || fwd_chunk_groups(pr, D, m_blocks, dev.num_sms) < pr.num_seqs * pr.Hq);
     const bool local = pr.wl >= 0;
-    if (dyn) return local ? run_fwd<D, NQ, BK, KST, true, true>(pr, out, lse, counter, dev, stream)
-                          : run_fwd<D, NQ, BK, KST, false, true>(pr, out, lse, counter, dev, stream);
-    return local ? run_fwd<D, NQ, BK, KST, true, false>(pr, out, lse, nullptr, dev, stream)
-                 : run_fwd<D, NQ, BK, KST, false, false>(pr, out, lse, nullptr, dev, stream);
+    auto run = [&](auto mode) {
+        constexpr int MODE = decltype(mode)::value;
+        if constexpr (MODE != kScorePlain)
+            return dyn ? run_fwd<D, NQ, BK, KST, true, true, MODE>(pr, out, lse, counter, dev, stream)
+                       : run_fwd<D, NQ, BK, KST, true, false, MODE>(pr, out, lse, nullptr, dev, stream);
+        else if (dyn)
+            return local ? run_fwd<D, NQ, BK, KST, true, true, MODE>(pr, out, lse, counter, dev, stream)
+                         : run_fwd<D, NQ, BK, KST, false, true, MODE>(pr, out, lse, counter, dev, stream);
+        else
+            return local ? run_fwd<D, NQ, BK, KST, true, false, MODE>(pr, out, lse, nullptr, dev, stream)
+                         : run_fwd<D, NQ, BK, KST, false, false, MODE>(pr, out, lse, nullptr, dev, stream);
+    };
+    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
 }
 
 int launch_fwd(const Problem& pr, void* out, float* lse, int* counter, const Device& dev, cudaStream_t stream) {

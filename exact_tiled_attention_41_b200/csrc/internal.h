@@ -31,7 +31,17 @@ struct Problem {
     // LSE addressing: index = b * lse_sB + h * lse_sH + tok_start * lse_sT + row
     long long lse_sB, lse_sH;
     int lse_sT;
+    // Score modifiers: cap * tanh(scale s / cap) - slope |i + Lk - Lq - j|; softcap = 0 and slopes = NULL
+    // leave the scores as they are.  Slopes: slopes[b * slope_sB + h] (slope_sB = 0: shared by the batch).
+    float softcap;
+    const float* slopes;
+    int slope_sB;
 };
+
+// The bit mask of score.cuh that a problem's modifiers ask for.
+inline int score_mode(float softcap, const float* slopes) {
+    return (softcap > 0.f ? 1 : 0) | (slopes != nullptr ? 2 : 0);
+}
 
 struct Device {
     int id;
@@ -99,6 +109,12 @@ struct KvCall {
     int B, Hq, Hkv, Sq, D;
     float scale;
     int causal, window_left, window_right, num_splits;
+    float softcap;                   // score modifiers as in Problem
+    const float* slopes;
+    int slope_sB;
+    const float* rotary_cos;         // [rotary_len, rotary_dim / 2], or NULL: q and k_new stay as they are
+    const float* rotary_sin;
+    int rotary_len, rotary_dim, rotary_interleaved;
 };
 
 int kvcache_validate(const KvCall& c, bool pointers);         // FA status, no CUDA calls
@@ -106,6 +122,22 @@ int kvcache_chunk(const KvCall& c, int num_sms);              // keys per split 
 int kvcache_chunk_limit(const KvCall& c);                     // keys one sequence can hold
 size_t kvcache_workspace_bytes(const KvCall& c, int chunk);   // float32 partial outputs and LSEs
 int kvcache_launch(const KvCall& c, int chunk, void* workspace, const Device& dev, cudaStream_t stream);
+
+// One rotary call; strides in values, dense [num_seqs, S, H, D] or packed [tokens, H, D] with cu_seqlens.
+struct RotaryCall {
+    const void* x;
+    void* y;
+    const float* cos;                // [seqlen_ro, rotary_dim / 2]
+    const float* sin;
+    const int32_t* cu_seqlens;       // device [num_seqs + 1] or NULL
+    const int32_t* offsets;          // device [num_seqs] or NULL
+    int offset, num_seqs, S, H, D, rotary_dim, seqlen_ro, interleaved, inverse;
+    long long tokens;
+    long long x_stride[3], y_stride[3];   // sequence, token, head
+};
+int launch_rotary(const RotaryCall& c, const Device& dev, cudaStream_t stream);
+int launch_rotary_table(float* cos, float* sin, int rows, int rotary_dim, const double* freq, float amplitude,
+                        cudaStream_t stream);
 
 int launch_wait_selftest(unsigned long long timeout_ns, const Device& dev, cudaStream_t stream);
 int launch_exp2_selftest(const float* x, float* y, int n, cudaStream_t stream);

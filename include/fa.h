@@ -212,8 +212,8 @@ FA_API int fa_fwd_kvcache(const void* q, const void* k_cache, const void* v_cach
                    void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /* ------------------------------------------------------------------------- KV-cache: append, pages, windows
- * fa_fwd_kvcache_ex: the rest of flash_attn_with_kvcache (README docstring),
- * without rotary embedding.  In order, on `stream`:
+ * fa_fwd_kvcache_ex: the rest of flash_attn_with_kvcache (README docstring);
+ * rotary positions are in fa_fwd_kvcache_mod below.  In order, on `stream`:
  *  1. If k_new / v_new [B, seqlen_new, Hkv, D] are given (both, seqlen_new > 0),
  *     they are written into k_cache / v_cache IN PLACE at logical rows
  *     cache_seqlens[b] .. cache_seqlens[b] + seqlen_new - 1 of sequence b.
@@ -249,6 +249,129 @@ FA_API int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const 
                              void* out, float* lse, int B, int Hq, int Hkv, int Sq, int D,
                              float softmax_scale, int causal, int window_left, int window_right, int num_splits,
                              void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* ------------------------------------------------------------------------- score modifiers
+ * The *_mod entry points are the *_ex calls with scores that are capped and / or
+ * biased (flash-attention README, flash_attn_func docstring: alibi_slopes;
+ * changelog 2.6: softcapping):
+ *     x_ij = softcap * tanh(softmax_scale * q_i . k_j / softcap)
+ *            - slope_h * |i + Sk - Sq - j|
+ * in place of softmax_scale * q_i . k_j, before mask and softmax; out, lse and the
+ * gradients are those of x.  (The README prints the bias; it names the cap without a
+ * formula, and the tanh above is the reading taken.)  The *_ex calls are these with
+ * softcap = 0 and alibi_slopes = NULL, and give the same bits.
+ *   softcap       0 = no cap; else positive and finite, at most 1e20, with
+ *                 1e-20 <= softmax_scale / softcap <= 1e20.
+ *   alibi_slopes  DEVICE float32, slope of query head h of sequence b at
+ *                 alibi_slopes[b * alibi_batch_stride + h], any finite values; NULL = no
+ *                 bias.  alibi_batch_stride is 0 (one set of Hq slopes for all
+ *                 sequences) or at least Hq.  Slopes are data: no gradient.
+ * Sk and Sq are the lengths of the sequence (varlen: of each; cache: keys attended to,
+ * and Sq).  Distances are formed in float32, exact up to 2^24 tokens.
+ * The backward needs the out and lse of the forward with the same modifiers.
+ * Workspaces and their sizes are those of the plain calls.
+ */
+FA_API int fa_fwd_mod(const void* q, const void* k, const void* v, void* out, float* lse,
+                      int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                      float softmax_scale, int causal, int window_left, int window_right,
+                      float softcap, const float* alibi_slopes, int alibi_batch_stride,
+                      void* workspace, size_t workspace_bytes, fa_stream_t stream);
+FA_API int fa_bwd_mod(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                      const float* lse, void* dq, void* dk, void* dv,
+                      int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                      float softmax_scale, int causal, int window_left, int window_right, int deterministic,
+                      float softcap, const float* alibi_slopes, int alibi_batch_stride,
+                      void* workspace, size_t workspace_bytes, fa_stream_t stream);
+FA_API int fa_varlen_fwd_mod(const void* q, const void* k, const void* v, void* out, float* lse,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                             int num_seqs, int max_seqlen_q, int max_seqlen_k, int total_q, int total_k,
+                             int Hq, int Hkv, int D, float softmax_scale, int causal,
+                             int window_left, int window_right,
+                             float softcap, const float* alibi_slopes, int alibi_batch_stride,
+                             void* workspace, size_t workspace_bytes, fa_stream_t stream);
+FA_API int fa_varlen_bwd_mod(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                             const float* lse, void* dq, void* dk, void* dv,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                             int num_seqs, int max_seqlen_q, int max_seqlen_k, int total_q, int total_k,
+                             int Hq, int Hkv, int D, float softmax_scale, int causal,
+                             int window_left, int window_right, int deterministic,
+                             float softcap, const float* alibi_slopes, int alibi_batch_stride,
+                             void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* fa_fwd_kvcache_mod: fa_fwd_kvcache_ex with score modifiers and rotary positions
+ * (README, flash_attn_with_kvcache docstring: rotary_cos, rotary_sin,
+ * rotary_interleaved).  With rotary_dim > 0, before the append and the attention:
+ *   - the new keys of sequence b are rotated at positions cache_seqlens[b] + token on
+ *     their way into the cache;
+ *   - its queries are rotated at cache_seqlens[b] + token under a causal mask or a
+ *     window, and all at cache_seqlens[b] otherwise (into the workspace; q itself is
+ *     not written).
+ * The result has the bits of fa_rotary on q and k_new followed by fa_fwd_kvcache_mod
+ * without rotary.  It needs k_new / v_new (as in the docstring) and tables of
+ * rotary_len rows, float32 [rotary_len][rotary_dim / 2], 16-byte aligned; rotary_dim
+ * a multiple of 16, at most D; rotary_interleaved as for fa_rotary.  A position at or
+ * past rotary_len records FA_ERR_INVALID_ARG in the device status word, and the row
+ * becomes zeros.  rotary_dim = 0 with NULL tables: no rotary.
+ */
+FA_API size_t fa_fwd_kvcache_mod_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
+                                                int max_blocks_per_seq, int num_splits, int rotary_dim);
+FA_API int fa_fwd_kvcache_mod(const void* q, void* k_cache, void* v_cache, const int32_t* cache_seqlens,
+                              const void* k_new, const void* v_new, int seqlen_new,
+                              const int32_t* cache_batch_idx, const int32_t* block_table, int max_blocks_per_seq,
+                              int cache_batch, int cache_capacity,
+                              void* out, float* lse, int B, int Hq, int Hkv, int Sq, int D,
+                              float softmax_scale, int causal, int window_left, int window_right, int num_splits,
+                              float softcap, const float* alibi_slopes, int alibi_batch_stride,
+                              const float* rotary_cos, const float* rotary_sin, int rotary_len, int rotary_dim,
+                              int rotary_interleaved, void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* ------------------------------------------------------------------------- rotary positions
+ * fa_rotary: rotates the first rotary_dim values of each head of x, in the pairs
+ * (2i, 2i + 1) (interleaved != 0) or (i, i + rotary_dim / 2) (0), i < rotary_dim / 2:
+ *     y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin
+ * with cos, sin from row `position` of the tables; the other values are copied.
+ * inverse != 0 rotates by the opposite angle, which is also the gradient: dx is the
+ * inverse rotation of dy.
+ *   x, y  bf16, [num_seqs, S, H, D], or [total, H, D] with cu_seqlens (DEVICE int32
+ *         [num_seqs + 1]); D in {64, 128, 256} innermost, the other strides given in
+ *         elements, multiples of 8 (the sequence stride is not used with cu_seqlens), so
+ *         that a slice of a packed projection can be rotated as it lies.
+ *   y may be x with the same strides (in place); other overlaps are not supported.
+ *   position of a token = its index in its sequence + seqlen_offsets[b] (DEVICE int32
+ *         [num_seqs], or NULL: + seqlen_offset).
+ *   rotary_cos, rotary_sin  float32 [rotary_len][rotary_dim / 2], 16-byte aligned;
+ *         rotary_dim a multiple of 16, at most D.
+ * A position outside the tables records FA_ERR_INVALID_ARG in the device status word, and
+ * the rotated values of the row become zeros.  Rows of y behind the last sequence of a packed
+ * batch are left as they are.  No workspace.
+ */
+FA_API int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rotary_sin,
+                     const int32_t* cu_seqlens, const int32_t* seqlen_offsets, int seqlen_offset,
+                     int num_seqs, int S, int total, int H, int D, int rotary_dim, int rotary_len,
+                     long long x_stride_seq, long long x_stride_tok, long long x_stride_head,
+                     long long y_stride_seq, long long y_stride_tok, long long y_stride_head,
+                     int interleaved, int inverse, fa_stream_t stream);
+
+/* fa_rotary_tables: row p, column i of the tables is amplitude * cos / sin (p * f_i),
+ * i < rotary_dim / 2, p < rotary_len, with f_i = base^(-2i / rotary_dim) scaled for contexts
+ * longer than the one a model was trained on (original_len):
+ *   FA_ROTARY_PLAIN     f_i
+ *   FA_ROTARY_LINEAR    f_i / factor (positions interpolated)
+ *   FA_ROTARY_BASE      f_i of the base  base * factor^(rotary_dim / (rotary_dim - 2)), so that
+ *                       the slowest pair is slowed by factor and the fastest not at all
+ *   FA_ROTARY_BY_PARTS  (1 - g) f_i / factor + g f_i, where r = original_len f_i / 2 pi is the
+ *                       number of rotations in the original context and
+ *                       g = clamp((r - low_rotations) / (high_rotations - low_rotations), 0, 1)
+ * Angles are reduced exactly, so far positions are as accurate as near ones (float32 rounding).
+ * base > 1; factor >= 1 unless PLAIN; BY_PARTS: original_len > 0 and
+ * 0 <= low_rotations < high_rotations.  rotary_dim a multiple of 16, at most 256.
+ */
+enum fa_rotary_scaling {
+    FA_ROTARY_PLAIN = 0, FA_ROTARY_LINEAR = 1, FA_ROTARY_BASE = 2, FA_ROTARY_BY_PARTS = 3
+};
+FA_API int fa_rotary_tables(float* rotary_cos, float* rotary_sin, int rotary_len, int rotary_dim, double base,
+                            int scaling, double factor, int original_len, double low_rotations,
+                            double high_rotations, double amplitude, fa_stream_t stream);
 
 /* ------------------------------------------------------------------------- merging partial attention results
  * fa_merge_lse: attention over the union of disjoint key sets from the results

@@ -1,0 +1,243 @@
+"""Capped and biased attention on the GPU against the fp64 oracle, element by element within the bounds that
+oracle/modifiers.py derives from the roundings: dense, packed and cached, forward and both backwards."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.modifiers as M
+from exact_tiled_attention_41_b200 import abi, attention as A, workloads as W
+from tests.gpu_helpers import f64
+
+pytestmark = pytest.mark.gpu
+
+NONE = (-1, -1)
+
+
+def slopes_of(Hq, B=None, kind="falling"):
+    s = torch.tensor([2.0 ** (-8.0 * (h + 1) / Hq) for h in range(Hq)])
+    if kind == "mixed":       # a zero, a negative and a steep one
+        s[0], s[-1] = 0.0, 2.5
+        if Hq > 2:
+            s[1] = -0.01
+    if B is not None:
+        s = torch.stack([s * (1.0 + 0.5 * b) for b in range(B)])
+    return s
+
+
+def compare(got, want, name):
+    g, w, tol = f64(got), want[name], want[name + "_tol"]
+    assert g.shape == w.shape
+    if name == "lse":
+        np.testing.assert_array_equal(np.isneginf(g), np.isneginf(w))
+        g, w = np.where(np.isneginf(w), 0.0, g), np.where(np.isneginf(w), 0.0, w)
+    assert np.isfinite(g).all(), name
+    over = np.abs(g - w) - tol
+    assert over.max(initial=-1.0) <= 0, f"{name}: off by {np.abs(g - w).flat[over.argmax()]:.3e}, allowed {tol.flat[over.argmax()]:.3e}"
+
+
+def check_dense(w, window, softcap, slopes, det=False, causal=None):
+    causal = w.causal if causal is None else causal
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    sl = None if slopes is None else slopes.cuda()
+    out, lse = A.flash_attn_func(t["q"], t["k"], t["v"], w.scale, causal, window, softcap, sl)
+    grads = A.flash_attn_backward(t["do"], t["q"], t["k"], t["v"], out, lse, w.scale, causal, window, det, softcap, sl)
+    torch.cuda.synchronize()
+    assert abi.fa_get_device_status() == 0
+    ref = M.attention(*(f64(w.tensors[n]) for n in ("q", "k", "v")), w.scale, causal, window, softcap,
+                      None if slopes is None else slopes.numpy(), f64(w.tensors["do"]))
+    for b, r in enumerate(ref):
+        for name, x in zip(("o", "lse", "dq", "dk", "dv"), (out, lse) + grads):
+            compare(x[b], r, name)
+
+
+MODS = [(20.0, None), (0.0, "falling"), (1.5, "mixed")]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap,kind", MODS)
+@pytest.mark.parametrize("Sq,Sk,causal,window,det", [
+    (1, 1, True, NONE, False),
+    (130, 130, True, NONE, False),
+    (300, 300, True, NONE, True),
+    (257, 97, True, NONE, False),          # rows without a key
+    (97, 389, False, NONE, True),
+    (200, 333, True, (70, -1), False),
+    (333, 200, False, (50, 30), False),
+])
+def test_dense(D, softcap, kind, Sq, Sk, causal, window, det):
+    w = W.dense(2, Sq, Sk, 4, 2, D, causal, seed=Sq + D)
+    check_dense(w, window, softcap, None if kind is None else slopes_of(4, kind=kind), det)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(6, 2), (5, 1), (3, 3)])
+def test_grouped_heads_and_slopes_of_each_sequence(Hq, Hkv):
+    w = W.dense(3, 140, 140, Hq, Hkv, 128, True, seed=Hq)
+    check_dense(w, NONE, 5.0, slopes_of(Hq, B=3))
+
+
+def test_scores_far_beyond_the_cap_and_around_every_tanh_branch():
+    # queries scaled so that |score| / cap runs from 0 to about 30
+    w = W.dense(1, 260, 260, 2, 2, 64, False, seed=9)
+    w.tensors["q"][:, 130:] *= 8.0
+    w.tensors["q"][:, 200:] *= 4.0
+    check_dense(w, NONE, 1.0, None)
+    check_dense(w, NONE, 1.0, None, det=True)
+
+
+@pytest.mark.parametrize("softcap,kind", MODS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_packed_batch_with_empty_sequences(D, softcap, kind):
+    lq, lk = [0, 1, 130, 257, 5, 0, 64], [3, 1, 130, 100, 300, 0, 65]
+    w = W.varlen(lq, lk, 4, 2, D, True, seed=D)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    slopes = None if kind is None else slopes_of(4, B=len(lq), kind=kind)
+    sl = None if slopes is None else slopes.cuda()
+    where = (t["cu_q"], t["cu_k"], max(lq), max(lk))
+    for causal, window, det in ((True, NONE, False), (False, (40, 20), True)):
+        out, lse = A.flash_attn_varlen_func(t["q"], t["k"], t["v"], *where, w.scale, causal, window, softcap, sl)
+        grads = A.flash_attn_varlen_backward(t["do"], t["q"], t["k"], t["v"], out, lse, *where, w.scale, causal, window,
+                                             det, softcap, sl)
+        torch.cuda.synchronize()
+        assert abi.fa_get_device_status() == 0
+        cq, ck = w.tensors["cu_q"].tolist(), w.tensors["cu_k"].tolist()
+        cut = lambda n, cu: [f64(w.tensors[n])[a:b] for a, b in zip(cu, cu[1:])]  # noqa: E731
+        ref = M.attention(cut("q", cq), cut("k", ck), cut("v", ck), w.scale, causal, window, softcap,
+                          None if slopes is None else slopes.numpy(), cut("do", cq))
+        for b, r in enumerate(ref):
+            for name, x in zip(("o", "dq", "dk", "dv"), (out,) + grads):
+                cu = cq if name in ("o", "dq") else ck
+                compare(x[cu[b]:cu[b + 1]], r, name)
+            compare(lse[:, cq[b]:cq[b + 1]], r, "lse")
+
+
+def test_no_modifier_gives_the_bits_of_the_plain_call():
+    w = W.dense(2, 300, 300, 4, 2, 128, True, seed=2)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    out, lse = A.flash_attn_func(t["q"], t["k"], t["v"], w.scale, True)
+    out0, lse0 = torch.empty_like(out), torch.empty_like(lse)
+    assert abi.fa_fwd_ex(t["q"], t["k"], t["v"], out0, lse0, 2, 4, 2, 300, 300, 128, w.scale, 1, -1, -1) == 0
+    assert torch.equal(out, out0) and torch.equal(lse, lse0)
+
+
+def test_both_backwards_give_the_same_dk_and_dv_and_the_deterministic_one_repeats():
+    for D in (64, 128, 256):
+        w = W.dense(2, 333, 333, 4, 2, D, True, seed=3)
+        t = {n: x.cuda() for n, x in w.tensors.items()}
+        sl = slopes_of(4).cuda()
+        out, lse = A.flash_attn_func(t["q"], t["k"], t["v"], w.scale, True, NONE, 3.0, sl)
+        args = (t["do"], t["q"], t["k"], t["v"], out, lse, w.scale, True, NONE)
+        a, b, c = (A.flash_attn_backward(*args, det, 3.0, sl) for det in (True, True, False))
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        assert torch.equal(a[1], c[1]) and torch.equal(a[2], c[2])
+
+
+def test_steep_slopes_over_a_long_context():
+    # each row sees a handful of keys; the far ones underflow, and the reference maximum must not suffer
+    w = W.dense(1, 1500, 1500, 2, 1, 64, True, seed=4)
+    for causal in (True, False):
+        check_dense(w, NONE, 0.0, torch.tensor([8.0, -0.05]), causal=causal)
+
+
+def test_captured_replayed_and_on_another_stream():
+    w = W.dense(2, 200, 200, 4, 2, 128, True, seed=5)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    sl = slopes_of(4).cuda()
+
+    def step():
+        out, lse = A.flash_attn_func(t["q"], t["k"], t["v"], w.scale, True, NONE, 4.0, sl)
+        return (out, lse) + A.flash_attn_backward(t["do"], t["q"], t["k"], t["v"], out, lse, w.scale, True, NONE, True, 4.0, sl)
+
+    want = [x.clone() for x in step()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = step()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    t["q"].mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    half = [x.clone() for x in got]
+    assert all(torch.equal(a, b) for a, b in zip(half, step()))
+    assert not torch.equal(half[0], want[0])
+
+
+def test_autograd_and_slopes_without_a_gradient():
+    w = W.dense(2, 130, 130, 4, 2, 64, True, seed=6)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    q, k, v = (t[n].requires_grad_() for n in "qkv")
+    sl = slopes_of(4)
+    out = A.FlashAttnFunction.apply(q, k, v, w.scale, True, NONE, True, 6.0, sl.cuda())
+    out.backward(t["do"])
+    ref = M.attention(*(f64(w.tensors[n]) for n in ("q", "k", "v")), w.scale, True, NONE, 6.0, sl.numpy(), f64(w.tensors["do"]))
+    for b, r in enumerate(ref):
+        compare(out[b], r, "o")
+        for name, x in (("dq", q), ("dk", k), ("dv", v)):
+            compare(x.grad[b], r, name)
+    with pytest.raises(ValueError):
+        A.FlashAttnFunction.apply(q, k, v, w.scale, True, NONE, True, 0.0, sl.cuda().requires_grad_())
+
+
+def test_bad_slopes_are_refused():
+    q = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16, device="cuda")
+    z = lambda *shape: torch.zeros(shape, device="cuda")  # noqa: E731
+    for bad, err in ((z(3), ValueError), (z(3, 4), ValueError), (z(4).half(), TypeError), (z(8)[::2], ValueError)):
+        with pytest.raises(err):
+            A.flash_attn_func(q, q, q, alibi_slopes=bad)
+    with pytest.raises(ValueError):
+        A.flash_attn_func(q, q, q, alibi_slopes=torch.zeros(4))
+    for cap in (-1.0, math.nan, math.inf):
+        with pytest.raises(abi.FAError):
+            A.flash_attn_func(q, q, q, softcap=cap)
+
+
+# ------------------------------------------------------------------------------------------- KV cache
+def check_cache(w, causal, window, softcap, slopes, num_splits=0):
+    t = w.tensors
+    dev = {n: x.cuda() for n, x in t.items()}
+    out, lse = A.flash_attn_with_kvcache(dev["q"], dev["k_cache"], dev["v_cache"], dev["cache_seqlens"], w.scale, causal,
+                                         num_splits, True, dev.get("k_new"), dev.get("v_new"), dev.get("cache_batch_idx"),
+                                         dev.get("block_table"), window, softcap, None if slopes is None else slopes.cuda())
+    torch.cuda.synchronize()
+    assert abi.fa_get_device_status() == 0
+    kc, vc = f64(dev["k_cache"]), f64(dev["v_cache"])       # after the append
+    sn = w.meta["seqlen_new"]
+    keys, vals = [], []
+    for b, n in enumerate(t["cache_seqlens"].tolist()):
+        n += sn
+        if w.meta["page"]:
+            rows = t["block_table"][b].long().numpy()
+            keys.append(kc[rows].reshape(-1, *kc.shape[2:])[:n])
+            vals.append(vc[rows].reshape(-1, *vc.shape[2:])[:n])
+        else:
+            keys.append(kc[b, :n])
+            vals.append(vc[b, :n])
+    ref = M.attention(list(f64(t["q"])), keys, vals, w.scale, causal, window, softcap,
+                      None if slopes is None else slopes.numpy())
+    for b, r in enumerate(ref):
+        compare(out[b], r, "o")
+        compare(lse[b], r, "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap,kind", MODS)
+@pytest.mark.parametrize("Sq,new,page,causal,window", [
+    (1, 0, 0, False, NONE), (1, 1, 256, True, NONE), (3, 3, 0, True, (100, -1)), (5, 2, 256, False, (33, 12)),
+])
+def test_cache(D, softcap, kind, Sq, new, page, causal, window):
+    lens = [0, 1, 63, 255, 256, 700]
+    w = W.kvcache_update(len(lens), Sq, 8, 2, D, 1024, lens, seqlen_new=new, page=page, seed=D + Sq)
+    slopes = None if kind is None else slopes_of(8, B=len(lens), kind=kind)
+    check_cache(w, causal, window, softcap, slopes)
+
+
+@pytest.mark.parametrize("num_splits", [1, 3, 16])
+def test_cache_does_not_depend_on_the_split(num_splits):
+    w = W.kvcache_update(2, 4, 7, 7, 128, 2048, [2044, 513], seqlen_new=4, seed=8)
+    check_cache(w, True, NONE, 8.0, slopes_of(7), num_splits)
