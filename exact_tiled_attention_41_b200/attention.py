@@ -32,7 +32,7 @@ from . import abi
 def _check(t: torch.Tensor, name: str, dtype=torch.bfloat16):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -57,7 +57,7 @@ def _on_device(fn):
     @functools.wraps(fn)
     def run(*args, **kwargs):
         t = args[0] if args else next(iter(kwargs.values()), None)
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(t.device):
                 return fn(*args, **kwargs)
         return fn(*args, **kwargs)
@@ -255,10 +255,11 @@ def rotary_tables(seqlen, rotary_dim, base=10000.0, scaling="none", factor=1.0, 
 
 def _rotary_strides(t, name):
     """(sequence, token, head) strides in elements; 0 where a dimension has one entry."""
-    if t.stride(-1) != 1:
+    *strides, last = t.stride()
+    if last != 1:
         raise ValueError(f"{name} must have its head dimension contiguous")
-    s = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
-    return s if t.dim() == 4 else [0] + s
+    s = [st if n > 1 else 0 for st, n in zip(strides, t.shape)]
+    return s if len(s) == 3 else [0] + s
 
 
 @_on_device
@@ -274,7 +275,7 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
     """
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor (no CPU path)")
     if x.dtype != torch.bfloat16:
         raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")

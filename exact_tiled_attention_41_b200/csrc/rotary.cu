@@ -19,78 +19,113 @@ struct RotaryParams {
     int num_seqs, S, H, rd, rows;   // rows of the tables
     long long tokens;
     long long x_sB, x_sT, x_sH, y_sB, y_sT, y_sH;   // strides in values; sB unused with cu
-    int inverse, copy_rest;
+    int inverse;
+    int items;                // threads per row: pieces (interleaved) or pairs of pieces (halves), and copied pieces
     int* status;
 };
 
-// The sequence of token `tok` of a packed batch: the last b with cu[b] <= tok (-1 before the first).
+// The sequence of token `tok` of a packed batch: the last b with cu[b] <= tok, -1 before the first; the whole warp
+// searches together, 32 entries at a time.
 __device__ __forceinline__ int find_seq(const int32_t* cu, int n, long long tok) {
-    int lo = -1, hi = n + 1;   // cu[lo] <= tok < cu[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= tok) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n + 1;
+    for (;;) {
+        const int step = (len + 31) / 32;
+        const bool below = lane * step < len && __ldg(cu + lo + lane * step) <= tok;
+        const int count = __popc(__ballot_sync(0xffffffffu, below));
+        if (count == 0) return -1;
+        lo += (count - 1) * step;
+        len = min(step, len - (count - 1) * step);
+        if (step == 1) return lo;
     }
-    return lo;
 }
 
-// One warp per token and block of heads; a lane takes one piece (or, for halves, the two pieces of 8 pairs).
-template <int D, bool INTER>
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryParams p) {
-    const int lane = threadIdx.x & 31;
-    const long long tok = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (tok >= p.tokens) return;
-    long long xt, yt;
-    long long pos;
-    int b;
-    if (p.cu != nullptr) {
-        b = find_seq(p.cu, p.num_seqs, tok);
-        if (b < 0 || b >= p.num_seqs) return;   // behind the last sequence: left as it was
-        pos = tok - __ldg(p.cu + b);
-        xt = tok * p.x_sT;
-        yt = tok * p.y_sT;
-    } else {
-        b = static_cast<int>(tok / p.S);
-        pos = tok % p.S;
-        xt = b * p.x_sB + pos * p.x_sT;
-        yt = b * p.y_sB + pos * p.y_sT;
-    }
-    pos += p.offsets != nullptr ? __ldg(p.offsets + b) : p.offset;
-    const bool bad = pos < 0 || pos >= p.rows;
-    if (bad && lane == 0) atomicCAS(p.status, 0, FA_ERR_INVALID_ARG);
+// A row is one head of one token.  p.items threads share a row: a thread takes the 16-byte piece of four
+// interleaved pairs, the two pieces of eight pairs of halves, or a piece that is only copied.  A block takes
+// consecutive rows (token by token, head by head), kRotRows of them per thread, whose loads are all in flight before
+// the first store: bound by HBM, it needs about 35 KB in flight per SM.  The cosines and sines of a
+// token are read once per head from L1 / L2, which is a third of the wavefronts and no HBM traffic.
+constexpr int kRotThreads = 256;
+constexpr int kRotRows = 2;
+
+template <bool INTER>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+    const int slots = kRotThreads / p.items;            // rows side by side
+    const int slot = threadIdx.x / p.items, item = threadIdx.x % p.items;
+    const long long row0 = static_cast<long long>(blockIdx.x) * (slots * kRotRows);
+    const long long tok0 = row0 / p.H;
+    const int h0 = static_cast<int>(row0 - tok0 * p.H);
     const int half = p.rd / 2;
-    const float* cr = p.cos + static_cast<size_t>(bad ? 0 : pos) * half;
-    const float* sr = p.sin + static_cast<size_t>(bad ? 0 : pos) * half;
-    const float sign = p.inverse ? -1.f : 1.f;
-    constexpr int PIECES = D / 8;
-    for (int idx = lane; idx < p.H * PIECES; idx += 32) {
-        const int h = idx / PIECES, d = (idx % PIECES) * 8;
-        const __nv_bfloat16* xr = p.x + xt + h * p.x_sH;
-        __nv_bfloat16* yr = p.y + yt + h * p.y_sH;
-        if (d >= p.rd) {
-            if (p.copy_rest) *reinterpret_cast<uint4*>(yr + d) = *reinterpret_cast<const uint4*>(xr + d);
-            continue;
-        }
-        if (bad) {
-            *reinterpret_cast<uint4*>(yr + d) = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        if constexpr (INTER) {
-            float4 c = __ldg(reinterpret_cast<const float4*>(cr + d / 2));
-            float4 s = __ldg(reinterpret_cast<const float4*>(sr + d / 2));
-            s = make_float4(s.x * sign, s.y * sign, s.z * sign, s.w * sign);
-            *reinterpret_cast<uint4*>(yr + d) = rot_interleaved(*reinterpret_cast<const uint4*>(xr + d), c, s);
-        } else if (d < half) {
-            float c[8], s[8];
-            load8(cr + d, c);
-            load8(sr + d, s);
+    const int turned = INTER ? p.rd / 8 : p.rd / 16;    // items of a row that rotate
+    const bool turn = item < turned;
+    const int d = turn ? item * 8 : p.rd + (item - turned) * 8;
+    const int ci = INTER ? d / 2 : d;                   // column of the tables
+    // the sequence of the block's first token; a row's own is at most a few further on
+    const int b0 = p.cu != nullptr ? find_seq(p.cu, p.num_seqs, tok0) : 0;
+
+    uint4 u[kRotRows], v[kRotRows];
+    const float *cr[kRotRows], *sr[kRotRows];
+    __nv_bfloat16* y[kRotRows];
+    bool live[kRotRows], bad[kRotRows];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] *= sign;
-            uint4 u = *reinterpret_cast<const uint4*>(xr + d), v = *reinterpret_cast<const uint4*>(xr + d + half);
-            rot_halves(u, v, c, s);
-            *reinterpret_cast<uint4*>(yr + d) = u;
-            *reinterpret_cast<uint4*>(yr + d + half) = v;
+    for (int k = 0; k < kRotRows; ++k) {
+        const int r = h0 + slot + k * slots;
+        const int dt = r / p.H, h = r - dt * p.H;
+        const long long tok = tok0 + dt;
+        live[k] = slot < slots && tok < p.tokens;
+        bad[k] = false;
+        if (!live[k]) continue;
+        int b;
+        long long pos, xo, yo;
+        if (p.cu != nullptr) {
+            b = b0;
+            while (b < p.num_seqs && __ldg(p.cu + b + 1) <= tok) ++b;
+            if (b < 0 || b >= p.num_seqs) {              // behind the last sequence: left as it was
+                live[k] = false;
+                continue;
+            }
+            pos = tok - __ldg(p.cu + b);
+            xo = tok * p.x_sT;
+            yo = tok * p.y_sT;
+        } else {
+            b = static_cast<int>(tok / p.S);
+            pos = tok - static_cast<long long>(b) * p.S;
+            xo = b * p.x_sB + pos * p.x_sT;
+            yo = b * p.y_sB + pos * p.y_sT;
         }
+        pos += p.offsets != nullptr ? __ldg(p.offsets + b) : p.offset;
+        bad[k] = pos < 0 || pos >= p.rows;
+        const size_t t = static_cast<size_t>(bad[k] ? 0 : pos) * half + ci;
+        cr[k] = p.cos + t;
+        sr[k] = p.sin + t;
+        const __nv_bfloat16* x = p.x + xo + h * p.x_sH + d;
+        y[k] = p.y + yo + h * p.y_sH + d;
+        u[k] = *reinterpret_cast<const uint4*>(x);
+        if (!INTER && turn) v[k] = *reinterpret_cast<const uint4*>(x + half);
+    }
+    const float sign = p.inverse ? -1.f : 1.f;
+#pragma unroll
+    for (int k = 0; k < kRotRows; ++k) {
+        if (!live[k]) continue;
+        if (turn) {
+            if (bad[k]) {
+                if (item == 0) atomicCAS(p.status, 0, FA_ERR_INVALID_ARG);
+                u[k] = v[k] = make_uint4(0, 0, 0, 0);
+            } else if constexpr (INTER) {
+                const float4 c = __ldg(reinterpret_cast<const float4*>(cr[k]));
+                const float4 s = __ldg(reinterpret_cast<const float4*>(sr[k]));
+                u[k] = rot_interleaved(u[k], c, make_float4(s.x * sign, s.y * sign, s.z * sign, s.w * sign));
+            } else {
+                float c[8], s[8];
+                load8(cr[k], c);
+                load8(sr[k], s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] *= sign;
+                rot_halves(u[k], v[k], c, s);
+            }
+            if (!INTER) *reinterpret_cast<uint4*>(y[k] + half) = v[k];
+        }
+        *reinterpret_cast<uint4*>(y[k]) = u[k];
     }
 }
 
@@ -116,16 +151,15 @@ int launch_rotary(const RotaryCall& c, const Device& dev, cudaStream_t stream) {
     p.y_sT = c.y_stride[1];
     p.y_sH = c.y_stride[2];
     p.inverse = c.inverse;
-    p.copy_rest = c.x != c.y;
+    p.items = (c.interleaved ? c.rotary_dim / 8 : c.rotary_dim / 16) + (c.x != c.y ? (c.D - c.rotary_dim) / 8 : 0);
     p.status = dev.status;
-    const long long blocks = (p.tokens + 7) / 8;
+    const long long per_block = kRotThreads / p.items * kRotRows;
+    const long long blocks = (p.tokens * p.H + per_block - 1) / per_block;
     if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    auto run = [&](auto kern) { kern<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p); };
-    switch (c.D) {
-        case 64: c.interleaved ? run(rotary_kernel<64, true>) : run(rotary_kernel<64, false>); break;
-        case 128: c.interleaved ? run(rotary_kernel<128, true>) : run(rotary_kernel<128, false>); break;
-        case 256: c.interleaved ? run(rotary_kernel<256, true>) : run(rotary_kernel<256, false>); break;
-        default: return FA_ERR_UNSUPPORTED;
+    if (c.interleaved) {
+        rotary_kernel<true><<<static_cast<unsigned>(blocks), kRotThreads, 0, stream>>>(p);
+    } else {
+        rotary_kernel<false><<<static_cast<unsigned>(blocks), kRotThreads, 0, stream>>>(p);
     }
     return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -143,17 +177,32 @@ struct TableParams {
     float amplitude;
 };
 
+// A thread owns four neighbouring pairs of a column block and walks down the rows: one 16-byte store to each table
+// per row, and the frequencies stay in registers.
+constexpr int kTableRows = 8;   // rows per thread
+
 __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant__ TableParams p) {
-    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= static_cast<long long>(p.rows) * p.half) return;
-    const unsigned pos = static_cast<unsigned>(i / p.half);
-    const int k = static_cast<int>(i % p.half);
-    const uint64_t frac = pos * p.turn[k];
-    const float x = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 4.656612873077393e-10f;   // 2^-31
-    float s, c;
-    sincospif(x, &s, &c);
-    p.cos[i] = c * p.amplitude;
-    p.sin[i] = s * p.amplitude;
+    const int groups = p.half >> 2;                    // rotary_dim % 16 == 0: half is a multiple of 8
+    const int per_block = 256 / groups;                // rows side by side in a block
+    const int r = threadIdx.x / groups, k = (threadIdx.x % groups) * 4;
+    if (r >= per_block) return;
+    uint64_t turn[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) turn[e] = p.turn[k + e];
+    long long pos = static_cast<long long>(blockIdx.x) * per_block * kTableRows + r;
+#pragma unroll
+    for (int i = 0; i < kTableRows; ++i, pos += per_block) {
+        if (pos >= p.rows) return;
+        float s[4], c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t frac = static_cast<uint32_t>(pos) * turn[e];
+            sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31
+        }
+        const float a = p.amplitude;
+        *reinterpret_cast<float4*>(p.cos + pos * p.half + k) = make_float4(c[0] * a, c[1] * a, c[2] * a, c[3] * a);
+        *reinterpret_cast<float4*>(p.sin + pos * p.half + k) = make_float4(s[0] * a, s[1] * a, s[2] * a, s[3] * a);
+    }
 }
 
 int launch_rotary_table(float* cos, float* sin, int rows, int rotary_dim, const double* freq, float amplitude,
@@ -168,8 +217,8 @@ int launch_rotary_table(float* cos, float* sin, int rows, int rotary_dim, const 
         const double t = freq[i] * 0.15915494309189533577;            // turns per position
         p.turn[i] = static_cast<uint64_t>(llrint(ldexp(t - rint(t), 63))) << 1;   // modulo one turn
     }
-    const long long n = static_cast<long long>(rows) * p.half;
-    rotary_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(p);
+    const int rows_per_block = 256 / (p.half / 4) * kTableRows;
+    rotary_table_kernel<<<(rows + rows_per_block - 1) / rows_per_block, 256, 0, stream>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
