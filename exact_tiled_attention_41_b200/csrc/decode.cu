@@ -277,8 +277,10 @@ __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
         }
         // ---- cap and bias
         if constexpr ((MODE & kScoreCap) != 0) {
-            cap_scores(sc[0], p.sc.in);
-            cap_scores(sc[1], p.sc.in);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[t][e] = tanh_mufu(sc[t][e] * p.sc.in);
         }
         if constexpr ((MODE & kScoreBias) != 0) {
             const float mul = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;

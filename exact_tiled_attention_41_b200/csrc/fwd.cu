@@ -521,8 +521,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 if constexpr ((MODE & kScoreBias) != 0) {
                     const float mul = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
                     const float d0 = static_cast<float>(row + (t.Lk - t.Lq) - kbase);   // distance of column 0
-#pragma unroll
-                    for (int c = 0; c < BK; ++c) s[c] = fmaf(s[c], mul, bias_log2(d0 - c, slope));
+                    bias_scores(s, mul, slope, d0, p.wr == 0);
                 }
                 const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
                 if (masked) {

@@ -45,7 +45,7 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, long long tok)
 // consecutive rows (token by token, head by head), kRotRows of them per thread, whose loads are all in flight before
 // the first store: bound by HBM, it needs about 35 KB in flight per SM.  The cosines and sines of a
 // token are read once per head from L1 / L2, which is a third of the wavefronts and no HBM traffic.
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 constexpr int kRotRows = 2;
 
 template <bool INTER>
@@ -186,18 +186,21 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant
     const int per_block = 256 / groups;                // rows side by side in a block
     const int r = threadIdx.x / groups, k = (threadIdx.x % groups) * 4;
     if (r >= per_block) return;
-    uint64_t turn[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) turn[e] = p.turn[k + e];
     long long pos = static_cast<long long>(blockIdx.x) * per_block * kTableRows + r;
+    uint64_t frac[4], step[4];   // fraction of a turn at pos, and from one row of the thread to its next
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        frac[e] = static_cast<uint32_t>(pos) * p.turn[k + e];
+        step[e] = static_cast<uint32_t>(per_block) * p.turn[k + e];
+    }
 #pragma unroll
     for (int i = 0; i < kTableRows; ++i, pos += per_block) {
         if (pos >= p.rows) return;
         float s[4], c[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint64_t frac = static_cast<uint32_t>(pos) * turn[e];
-            sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31
+            sincospif(static_cast<float>(static_cast<int32_t>(frac[e] >> 32)) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31
+            frac[e] += step[e];
         }
         const float a = p.amplitude;
         *reinterpret_cast<float4*>(p.cos + pos * p.half + k) = make_float4(c[0] * a, c[1] * a, c[2] * a, c[3] * a);
