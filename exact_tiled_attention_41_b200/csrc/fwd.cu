@@ -217,13 +217,85 @@ __host__ __device__ constexpr int fma_exp_every(int D) {
 }
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// A cap beyond this needs a running maximum: 55 log2(e) < 80.
+constexpr float kMaxFixedCap = 55.f;
+constexpr int kScoreWide = 4;   // mode bit: a cap beyond kMaxFixedCap
+__host__ __device__ constexpr bool fixed_reference(int mode) { return (mode & kScoreCap) && !(mode & kScoreWide); }
+
+// One tile of a row against its fixed reference: P = exp2(c2 tanh(in s) + bias - reference) for the BK scores at
+// tS, written over them as packed bf16; returns the row's sum.  Columns lo .. hi are allowed (masked: some are
+// not); column c lies at distance d0 - c from the row, and the reference is the bias at distance d_ref.
+template <int BK, int MODE>
+__device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& sc, float c2, float slope, int d0, int d_ref,
+                                               bool past, bool masked, int lo, int hi) {
+    const float2 in2 = splat2(sc.in), c2v = splat2(c2);
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+    uint32_t s[2][32];
+    tmem_ld32(tS, s[0]);
+#pragma unroll 1
+    for (int cc = 0; cc < BK / 32; cc += 2) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int c0 = (cc + half) * 32;
+            tmem_ld_wait_tie(s[half]);
+            // the next 32 columns load meanwhile; P of columns c0 .. goes to the words c0 / 2 .., read before
+            if (c0 + 32 < BK) tmem_ld32(tS + c0 + 32, s[half ^ 1]);
+            float (&x)[32] = reinterpret_cast<float (&)[32]>(s[half]);
+            const float most = max_abs(x) * sc.in;
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] = (c0 + c >= lo && c0 + c <= hi) ? x[c] : -INFINITY;
+            }
+            // the bias less the reference: linear in the column on either side of the diagonal, step c + base
+            const int dc = d0 - c0;
+            bool across = false;
+            float step = 0.f, base = 0.f;
+            if constexpr ((MODE & kScoreBias) != 0) {
+                const bool behind = past || __all_sync(0xffffffffu, dc >= 31);
+                across = !behind && !__all_sync(0xffffffffu, dc <= 0);
+                step = behind ? slope : -slope;
+                base = behind ? -slope * static_cast<float>(dc - d_ref) : slope * static_cast<float>(dc + d_ref);
+            }
+            uint32_t pk[16];
+            auto pairs = [&](auto range, auto bias) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 t = cap_pair<decltype(range)::value>(make_float2(x[2 * e], x[2 * e + 1]), in2);
+                    const float2 y = (MODE & kScoreBias) ? ffma2(t, c2v, make_float2(bias(2 * e), bias(2 * e + 1))) : fmul2(t, c2v);
+                    const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                    if (e & 1) sum1 = fadd2(sum1, pr); else sum0 = fadd2(sum0, pr);
+                    pk[e] = pack_bf16x2(pr.x, pr.y);
+                }
+            };
+            if (across) {
+                const float from = static_cast<float>(dc), ref = slope * static_cast<float>(d_ref);
+                pairs(std::integral_constant<int, kTanhAny>{}, [&](int c) { return fmaf(-slope, fabsf(from - c), ref); });
+            } else {
+                with_tanh_range(most, [&](auto range) {
+                    pairs(range, [&](int c) { return fmaf(step, static_cast<float>(c), base); });
+                });
+            }
+            tmem_st16(tS + c0 / 2, pk);
+        }
+    }
+    const float2 sum = fadd2(sum0, sum1);
+    return sum.x + sum.y;
+}
+
 // DYN: units come from p.counter through the shared-memory feed (varlen batches, head chunks sized for
 // L2); otherwise each role walks the static boustrophedon deal itself (dense problems whose K and V fit
 // L2: the static deal is balanced there, and the feed's per-unit hand-off measured 2-3 % slower).
-// MODE: score modifiers (score.cuh).  With any, KV tiles are visited last tile first: under a causal mask
-// and a distance bias the nearest keys then set the row's reference maximum at once, where the other
-// order raises it (and rescales O) at nearly every tile of a steep head.  One order for all modifiers keeps
-// the instances few; they use the LOCAL tile ranges whatever the mask.
+// MODE: score modifiers (score.cuh).
+//  * Capped scores lie within +-cap, so unless the cap is beyond kMaxFixedCap no running maximum is needed: every row is
+//    taken against a fixed reference, the largest bias among its allowed keys (0 without a bias).  The scores
+//    above it are at most cap log2(e) <= 80, and the key with that bias lies at -80 or more: P, the sums and O stay
+//    far inside fp32 and bf16 range, and the result is the same softmax (it does not depend on the reference).
+//    That leaves one pass over the scores, taken 32 columns at a time from tensor memory, in which the tanh
+//    and exponent arithmetic of the FMA pipe runs beside the exponentials.
+//  * Otherwise (kScoreWide, or a bias alone) the row keeps its reference maximum as without modifiers, and KV tiles are
+//    visited last tile first: under a causal mask and a distance bias the nearest keys then set the
+//    maximum at once, where the other order raises it (and rescales O) at nearly every tile of a steep head.
+//    These instances use the LOCAL tile ranges whatever the mask.
 template <int D, int NQ, int BK, int KST, bool LOCAL, bool DYN, int MODE>
 __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -231,7 +303,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
     using C = FwdCfg<D, NQ, BK, KST>;
     constexpr int BM = C::BM;
     constexpr int ROWS = BM * NQ;
-    constexpr bool REV = MODE != kScorePlain;
+    constexpr bool FIXED = fixed_reference(MODE), REV = MODE != kScorePlain && !FIXED;
     static_assert(LOCAL || !REV, "the turned tile ranges need lo[]");
 
     extern __shared__ uint8_t smem_raw[];
@@ -463,9 +535,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
         const uint32_t lane_base = tmem_lane_base(wq);
         const uint32_t tS = tmem + lane_base + C::S_COL(i);
         const uint32_t tO = tmem + lane_base + C::O_COL(i);
-        // scores enter the exponentials as s * c2: with a bias s is already in log2 units, with a cap alone
-        // s is the tanh
-        const float c2 = (MODE & kScoreBias) ? 1.f : (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
+        // scores enter the exponentials as s * c2; with a cap s is the tanh
+        const float c2 = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
         uint32_t s_it = 0, pv_total = 0;
         bool ok = true;
         for (uint32_t fi = 0; ok; ++fi) {
@@ -497,14 +568,26 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             int key_lo = 0, key_hi = t.Lk - 1;
             if (LOCAL && (!REV || p.wl >= 0)) key_lo = max(0, row + (t.Lk - t.Lq) - p.wl);
             if (p.wr >= 0) key_hi = min(key_hi, row + (t.Lk - t.Lq) + p.wr);
-            float slope = 0.f;
-            if constexpr ((MODE & kScoreBias) != 0) slope = slope_log2(p.sc, t.b, t.h);
+            float slope = 0.f;   // in log2 units (FIXED), or in the unit of s
+            if constexpr ((MODE & kScoreBias) != 0) slope = slope_log2(p.sc, t.b, t.h) / (FIXED ? 1.f : c2);
+            const int at = row + (t.Lk - t.Lq);   // the row's place among the keys
+            // FIXED: distance of the allowed key with the largest bias (the nearest, or the farthest for a negative
+            // slope)
+            int d_ref = 0;
+            if constexpr (FIXED && (MODE & kScoreBias) != 0)
+                d_ref = slope >= 0.f ? max(0, max(key_lo - at, at - key_hi)) : max(abs(at - key_lo), abs(at - key_hi));
             float m_ref = -INFINITY;
             float l = 0.f;
             for (int j = 0; j < n_mine; ++j) {
                 if (!mbar_wait(s_full(i), s_it & 1, w)) { ok = false; break; }
                 ++s_it;
                 tc_fence_after();
+                const int kbase = unit_tile<LOCAL, REV>(t, lo_i + j) * BK;
+                const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
+                if constexpr (FIXED) {
+                    l += softmax_fixed<BK, MODE>(tS, p.sc, c2, slope, at - kbase, d_ref, p.wr == 0, masked, key_lo - kbase,
+                                                 key_hi - kbase);
+                } else {
                 float s[BK];
                 {
                     // the whole row in one round trip: BK/32 loads, one wait
@@ -516,14 +599,10 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
 #pragma unroll
                     for (int cc = 1; cc < BK / 32; ++cc) reg_tie(*reinterpret_cast<uint32_t(*)[32]>(sr + cc * 32));
                 }
-                const int kbase = unit_tile<LOCAL, REV>(t, lo_i + j) * BK;
+                float shift = 0.f;   // the row's part of the bias
                 if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc.in);
-                if constexpr ((MODE & kScoreBias) != 0) {
-                    const float mul = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
-                    const float d0 = static_cast<float>(row + (t.Lk - t.Lq) - kbase);   // distance of column 0
-                    bias_scores(s, mul, slope, d0, p.wr == 0);
-                }
-                const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
+                if constexpr ((MODE & kScoreBias) != 0)
+                    shift = bias_scores(s, slope, static_cast<float>(at - kbase), p.wr == 0);
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < BK; ++c)
@@ -532,7 +611,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int c = 4; c < BK; c += 2) mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], s[c], s[c + 1]);
-                const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                if constexpr ((MODE & kScoreBias) != 0) mt += shift;
                 const bool need = (mt - m_ref) * c2 > kDeferLog2;   // NaN (both -inf) -> false
                 if (__any_sync(0xffffffffu, need)) {
                     const float m_new = fmaxf(m_ref, mt);
@@ -566,7 +646,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                     l *= alpha;
                     m_ref = m_new;
                 }
-                const float ms = (m_ref == -INFINITY) ? 0.f : m_ref * c2;
+                const float ms = (m_ref == -INFINITY) ? 0.f : (MODE & kScoreBias) ? (m_ref - shift) * c2 : m_ref * c2;
                 const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
                 // exp(scale * s - scale * m) as exp2 of one fused multiply-add per pair; on tiles
@@ -594,6 +674,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 {
                     const float2 sm = fadd2(sum0, sum1);
                     l += sm.x + sm.y;
+                }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -623,7 +704,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                     for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                 }
             }
-            if (valid) *lse_ptr = l > 0.f ? (m_ref * c2 + log2f(l)) * kLn2 : -INFINITY;
+            const float ref = FIXED ? -slope * d_ref : m_ref * c2;
+            if (valid) *lse_ptr = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             tc_fence_before();
         }
     }
@@ -730,7 +812,7 @@ static int run_fwd_d(const Problem& pr, void* out, float* lse, int* counter, con
     const bool local = pr.wl >= 0;
     auto run = [&](auto mode) {
         constexpr int MODE = decltype(mode)::value;
-        if constexpr (MODE != kScorePlain)
+        if constexpr (MODE != kScorePlain && !fixed_reference(MODE))
             return dyn ? run_fwd<D, NQ, BK, KST, true, true, MODE>(pr, out, lse, counter, dev, stream)
                        : run_fwd<D, NQ, BK, KST, true, false, MODE>(pr, out, lse, nullptr, dev, stream);
         else if (dyn)
@@ -740,7 +822,11 @@ static int run_fwd_d(const Problem& pr, void* out, float* lse, int* counter, con
             return local ? run_fwd<D, NQ, BK, KST, true, false, MODE>(pr, out, lse, nullptr, dev, stream)
                          : run_fwd<D, NQ, BK, KST, false, false, MODE>(pr, out, lse, nullptr, dev, stream);
     };
-    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
+    const int mode = score_mode(pr.softcap, pr.slopes);
+    if ((mode & kScoreCap) && pr.softcap > kMaxFixedCap)
+        return (mode & kScoreBias) ? run(std::integral_constant<int, kScoreCap | kScoreBias | kScoreWide>{})
+                                   : run(std::integral_constant<int, kScoreCap | kScoreWide>{});
+    return with_score_mode(mode, run);
 }
 
 int launch_fwd(const Problem& pr, void* out, float* lse, int* counter, const Device& dev, cudaStream_t stream) {

@@ -58,59 +58,69 @@ __device__ __forceinline__ float tanh_mufu(float x) {
     return fmaf(-2.f, rcp_approx(1.f + e), 1.f);
 }
 
-// tanh of a pair on the FMA pipe, x p(x^2) with p of the smallest maximum relative error on its range
-// (exact_tiled_attention_41_b200/fit_tanh_poly.py prints the coefficients): within 2e-7 relative.
 __device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ float2 tanh_half(float2 x) {   // |x| <= 1/2
-    const float2 u = fmul2(x, x);
-    float2 p = ffma2(splat2(0.0171350036f), u, splat2(-0.0529860742f));
-    p = ffma2(p, u, splat2(0.133247793f));
-    p = ffma2(p, u, splat2(-0.333330691f));
-    p = ffma2(p, u, splat2(1.0f));
-    return fmul2(p, x);
+// tanh(in * s) of a pair of raw scores, by the range of the arguments: x p(x^2) on the FMA pipe, with p of the
+// smallest maximum relative error on its range (exact_tiled_attention_41_b200/fit_tanh_poly.py prints the
+// coefficients; within 5e-7 relative for |x| <= 1/4, 2e-7 up to 1), or the multi-function unit.  A masked score, -inf,
+// stays -inf: the polynomials' leading coefficients are positive.
+// The coefficients stand in constant memory, doubled for the packed FMA.
+#define FA_2(v) {v, v}
+static __constant__ float2 kTanh2[3] = {FA_2(0.12841614f), FA_2(-0.33321908f), FA_2(0.9999996f)};
+static __constant__ float2 kTanh4[5] = {FA_2(0.0171350036f), FA_2(-0.0529860742f), FA_2(0.133247793f),
+                                        FA_2(-0.333330691f), FA_2(1.0f)};
+static __constant__ float2 kTanh6[7] = {FA_2(0.0010410226f), FA_2(-0.00620337902f), FA_2(0.0202899799f),
+                                        FA_2(-0.0534570292f), FA_2(0.13325204f), FA_2(-0.333328396f), FA_2(0.99999994f)};
+#undef FA_2
+enum TanhRange { kTanhQuarter, kTanhHalf, kTanhOne, kTanhAny };
+
+template <int RANGE>
+__device__ __forceinline__ float2 cap_pair(float2 s, float2 in) {
+    const float2 x = fmul2(s, in);
+    if constexpr (RANGE == kTanhAny) {
+        return make_float2(s.x == -INFINITY ? -INFINITY : tanh_mufu(x.x), s.y == -INFINITY ? -INFINITY : tanh_mufu(x.y));
+    } else {
+        const float2 u = fmul2(x, x);
+        constexpr int DEG = RANGE == kTanhQuarter ? 2 : RANGE == kTanhHalf ? 4 : 6;
+        const float2* c = RANGE == kTanhQuarter ? kTanh2 : RANGE == kTanhHalf ? kTanh4 : kTanh6;
+        float2 p = ffma2(c[0], u, c[1]);
+#pragma unroll
+        for (int i = 2; i <= DEG; ++i) p = ffma2(p, u, c[i]);
+        return fmul2(p, x);
+    }
 }
 
-__device__ __forceinline__ float2 tanh_one(float2 x) {    // |x| <= 1
-    const float2 u = fmul2(x, x);
-    float2 p = ffma2(splat2(0.0010410226f), u, splat2(-0.00620337902f));
-    p = ffma2(p, u, splat2(0.0202899799f));
-    p = ffma2(p, u, splat2(-0.0534570292f));
-    p = ffma2(p, u, splat2(0.13325204f));
-    p = ffma2(p, u, splat2(-0.333328396f));
-    p = ffma2(p, u, splat2(0.99999994f));
-    return fmul2(p, x);
+// Calls run(std::integral_constant<int, range>) for the smallest range that holds every argument of the warp
+// (most: the largest |argument| of the thread).  The softmax already keeps the multi-function unit busy with one
+// exponential per score, and a tanh there costs two more results, while the FMA pipe has room; with a cap
+// well above the scores, as caps are chosen, every block of scores takes one of the first ranges.
+template <typename F>
+__device__ __forceinline__ void with_tanh_range(float most, F&& run) {
+    if (__all_sync(0xffffffffu, most <= 0.25f)) run(std::integral_constant<int, kTanhQuarter>{});
+    else if (__all_sync(0xffffffffu, most <= 0.5f)) run(std::integral_constant<int, kTanhHalf>{});
+    else if (__all_sync(0xffffffffu, most <= 1.0f)) run(std::integral_constant<int, kTanhOne>{});
+    else run(std::integral_constant<int, kTanhAny>{});
 }
 
-// s <- tanh(in * s) for a thread's block of raw scores.  The softmax already keeps the multi-function unit busy with
-// one exponential per score, and a tanh there costs two more results; the FMA pipe has room.  So the warp takes
-// a polynomial whenever all its arguments are within its range (with a cap well above the scores, as caps are
-// chosen, that is every block), and the multi-function unit otherwise.
 template <int N>
-__device__ __forceinline__ void cap_scores(float (&s)[N], float in) {
+__device__ __forceinline__ float max_abs(const float (&s)[N]) {
     float m[2] = {fabsf(s[0]), fabsf(s[1])};
 #pragma unroll
     for (int e = 2; e < N; e += 2) m[(e >> 1) & 1] = max3f(m[(e >> 1) & 1], fabsf(s[e]), fabsf(s[e + 1]));
-    const float most = fmaxf(m[0], m[1]) * in;
-    const float2 in2 = splat2(in);
-    if (__all_sync(0xffffffffu, most <= 0.5f)) {
+    return fmaxf(m[0], m[1]);
+}
+
+// s <- tanh(in * s) for a thread's block of raw scores
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&s)[N], float in) {
+    with_tanh_range(max_abs(s) * in, [&](auto range) {
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-            const float2 t = tanh_half(fmul2(make_float2(s[e], s[e + 1]), in2));
+            const float2 t = cap_pair<decltype(range)::value>(make_float2(s[e], s[e + 1]), splat2(in));
             s[e] = t.x;
             s[e + 1] = t.y;
         }
-    } else if (__all_sync(0xffffffffu, most <= 1.0f)) {
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-            const float2 t = tanh_one(fmul2(make_float2(s[e], s[e + 1]), in2));
-            s[e] = t.x;
-            s[e + 1] = t.y;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) s[e] = tanh_mufu(s[e] * in);
-    }
+    });
 }
 template <int N>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float in) {
@@ -125,20 +135,22 @@ __device__ __forceinline__ float slope_log2(const ScoreParams& sc, int b, int h)
 // bias (log2 units) at signed distance d: -slope |d|.  Distances are formed in fp32, exact up to 2^24 tokens.
 __device__ __forceinline__ float bias_log2(float d, float slope) { return -slope * fabsf(d); }
 
-// s <- mul s + bias for a thread's row of scores, column c at distance d0 - c.  Where the warp's columns all lie on one
-// side of the diagonal (past: every column that the mask keeps does) the bias is one FMA, without it three
-// operations.
+// Adds the bias to a thread's row of scores, column c at distance d0 - c; slope in the unit of s.  Where the
+// warp's columns all lie on one side of the diagonal (past: every column that the mask keeps does) the bias is
+// linear in c, so only its column part is added, one FMA per score, and the row's part is returned; across
+// the diagonal the whole bias is added and 0 returned.
 template <int N>
-__device__ __forceinline__ void bias_scores(float (&s)[N], float mul, float slope, float d0, bool past) {
+__device__ __forceinline__ float bias_scores(float (&s)[N], float slope, float d0, bool past) {
     const bool behind = past || __all_sync(0xffffffffu, d0 >= N - 1);
     if (behind || __all_sync(0xffffffffu, d0 <= 0.f)) {
-        const float step = behind ? slope : -slope, base = -step * d0;
+        const float step = behind ? slope : -slope;
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], mul, fmaf(step, static_cast<float>(c), base));
-    } else {
-#pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], mul, bias_log2(d0 - c, slope));
+        for (int c = 1; c < N; ++c) s[c] = fmaf(step, static_cast<float>(c), s[c]);
+        return -step * d0;
     }
+#pragma unroll
+    for (int c = 0; c < N; ++c) s[c] = fmaf(-slope, fabsf(d0 - c), s[c]);
+    return 0.f;
 }
 
 // gradient of the raw scores from that of the capped ones: ds (1 - t^2), t the tanh

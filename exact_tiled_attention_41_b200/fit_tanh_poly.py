@@ -4,14 +4,14 @@
 
 tanh is odd, so tanh(x) = x p(x^2); p is fitted to tanh(sqrt(u)) / sqrt(u) on u in [0, R^2] with the smallest
 maximum *relative* error (Remez exchange: equioscillation of p(u) sqrt(u) / tanh(sqrt(u)) - 1 at degree + 2 points).
-Two ranges are used: degree 4 for |x| <= 1/2 and degree 6 for |x| <= 1.  The script prints the coefficients (highest
+Three ranges are used: degree 2 for |x| <= 1/4, degree 4 for |x| <= 1/2 and degree 6 for |x| <= 1.  The script prints the coefficients (highest
 degree first, as Horner's rule in csrc/score.cuh uses them) and the worst relative error of the fp32 evaluation.
 A CPU test re-runs the fit and compares it with the header.
 """
 
 import numpy as np
 
-RANGES = ((0.5, 4), (1.0, 6))
+RANGES = ((0.25, 2), (0.5, 4), (1.0, 6))
 
 
 def _target(u):
