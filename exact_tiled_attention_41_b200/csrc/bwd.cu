@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(512, 1)
                     tmem_ld32(tmem + lb + C::COL_DP + 64 * gq + 32 * half, dh);
                     tmem_ld_wait_tie(sh);
                     reg_tie(dh);
-                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc.in);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc);
                     uint32_t pp[16], dd[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_ld32(tmem + lb + C::COL_DP(gb) + 32 * half, dh);
                         tmem_ld_wait_tie(sh);
                         reg_tie(dh);
-                        if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc.in);
+                        if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc);
                         uint32_t pp[16], dd[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {

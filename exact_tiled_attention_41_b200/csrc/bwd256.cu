@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(512, 1)
                 tmem_ld32(tmem + lb + C::COL_DP + 32 * gq, da);
                 tmem_ld_wait_tie(sa);
                 reg_tie(da);
-                if constexpr ((MODE & kScoreCap) != 0) cap_scores(sa, p.sc.in);
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores(sa, p.sc);
                 float slope = 0.f, d0 = 0.f;   // distance of the warpgroup's first query column from the key
                 if constexpr ((MODE & kScoreBias) != 0) {
                     slope = slope_log2(p.sc, t.b, t.hk * G + it / t.n_m);

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(384, 1)
                     uint32_t sv[32];
                     tmem_ld32(tS + cc * 32, sv);
                     tmem_ld_wait_tie(sv);
-                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sv, p.sc.in);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sv, p.sc);
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {

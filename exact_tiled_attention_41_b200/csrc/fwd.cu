@@ -226,9 +226,8 @@ __host__ __device__ constexpr bool fixed_reference(int mode) { return (mode & kS
 // tS, written over them as packed bf16; returns the row's sum.  Columns lo .. hi are allowed (masked: some are
 // not); column c lies at distance d0 - c from the row, and the reference is the bias at distance d_ref.
 template <int BK, int MODE>
-__device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& sc, float c2, float slope, int d0, int d_ref,
+__device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& sc, float slope, int d0, int d_ref,
                                                bool past, bool masked, int lo, int hi) {
-    const float2 in2 = splat2(sc.in), c2v = splat2(c2);
     float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
     uint32_t s[2][32];
     tmem_ld32(tS, s[0]);
@@ -241,7 +240,7 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
             // the next 32 columns load meanwhile; P of columns c0 .. goes to the words c0 / 2 .., read before
             if (c0 + 32 < BK) tmem_ld32(tS + c0 + 32, s[half ^ 1]);
             float (&x)[32] = reinterpret_cast<float (&)[32]>(s[half]);
-            const float most = max_abs(x) * sc.in;
+            const float most = max_abs(x);
             if (masked) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c) x[c] = (c0 + c >= lo && c0 + c <= hi) ? x[c] : -INFINITY;
@@ -260,8 +259,8 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
             auto pairs = [&](auto range, auto bias) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float2 t = cap_pair<decltype(range)::value>(make_float2(x[2 * e], x[2 * e + 1]), in2);
-                    const float2 y = (MODE & kScoreBias) ? ffma2(t, c2v, make_float2(bias(2 * e), bias(2 * e + 1))) : fmul2(t, c2v);
+                    const float2 b = (MODE & kScoreBias) ? make_float2(bias(2 * e), bias(2 * e + 1)) : splat2(0.f);
+                    const float2 y = cap_pair_log2<decltype(range)::value>(make_float2(x[2 * e], x[2 * e + 1]), sc, b);
                     const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                     if (e & 1) sum1 = fadd2(sum1, pr); else sum0 = fadd2(sum0, pr);
                     pk[e] = pack_bf16x2(pr.x, pr.y);
@@ -271,7 +270,7 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
                 const float from = static_cast<float>(dc), ref = slope * static_cast<float>(d_ref);
                 pairs(std::integral_constant<int, kTanhAny>{}, [&](int c) { return fmaf(-slope, fabsf(from - c), ref); });
             } else {
-                with_tanh_range(most, [&](auto range) {
+                with_tanh_range(most, sc, [&](auto range) {
                     pairs(range, [&](int c) { return fmaf(step, static_cast<float>(c), base); });
                 });
             }
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 const int kbase = unit_tile<LOCAL, REV>(t, lo_i + j) * BK;
                 const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
                 if constexpr (FIXED) {
-                    l += softmax_fixed<BK, MODE>(tS, p.sc, c2, slope, at - kbase, d_ref, p.wr == 0, masked, key_lo - kbase,
+                    l += softmax_fixed<BK, MODE>(tS, p.sc, slope, at - kbase, d_ref, p.wr == 0, masked, key_lo - kbase,
                                                  key_hi - kbase);
                 } else {
                 float s[BK];
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                     for (int cc = 1; cc < BK / 32; ++cc) reg_tie(*reinterpret_cast<uint32_t(*)[32]>(sr + cc * 32));
                 }
                 float shift = 0.f;   // the row's part of the bias
-                if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc.in);
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc);
                 if constexpr ((MODE & kScoreBias) != 0)
                     shift = bias_scores(s, slope, static_cast<float>(at - kbase), p.wr == 0);
                 if (masked) {

@@ -19,15 +19,39 @@ namespace fa {
 // Score mode of a kernel instance, a bit mask; 0 leaves the kernels as they are without modifiers.
 constexpr int kScorePlain = 0, kScoreCap = 1, kScoreBias = 2;
 
+// Coefficients of the tanh polynomials, see cap_pair below.
+#define FA_TANH2 {0.12841614f, -0.33321908f, 0.9999996f}
+#define FA_TANH4 {0.0171350036f, -0.0529860742f, 0.133247793f, -0.333330691f, 1.0f}
+#define FA_TANH6 {0.0010410226f, -0.00620337902f, 0.0202899799f, -0.0534570292f, 0.13325204f, -0.333328396f, 0.99999994f}
+
 struct ScoreParams {
     float in;             // scale / cap: raw score -> argument of the tanh
     float out_log2;       // cap * log2(e): tanh -> score in log2 units
     const float* slopes;  // [Hq] (slope_sB = 0) or [B][Hq] (slope_sB = Hq)
     int slope_sB;
+    // The tanh polynomials (kTanh2, kTanh4) in the raw score, with both factors in the coefficients (each
+    // doubled for the packed FMA): out_log2 tanh(in s) = s (fold[0] w^n + ... + fold[n]), w = s^2, for |s| up to
+    // limit[range]; limit[2]: |in s| <= 1.
+    float2 fold2[3], fold4[5];
+    float limit[3];
 };
 
 inline ScoreParams score_params(float scale, float softcap, const float* slopes, int slope_sB) {
-    return {softcap > 0.f ? scale / softcap : 0.f, softcap * 1.4426950408889634f, slopes, slope_sB};
+    ScoreParams sc = {softcap > 0.f ? scale / softcap : 0.f, softcap * 1.4426950408889634f, slopes, slope_sB};
+    if (softcap > 0.f) {
+        // in^9 stays a normal float for in >= 2^-13; a smaller one (no usual scale and cap) does without the folded form
+        const bool fits = sc.in >= 0x1p-13f && sc.in <= 0x1p13f;
+        const double in = sc.in, c2[3] = FA_TANH2, c4[5] = FA_TANH4;
+        double f = in * sc.out_log2;
+        for (int k = 0; k < 5; ++k, f *= in * in) {
+            if (k < 3) sc.fold2[2 - k] = make_float2(static_cast<float>(c2[2 - k] * f), static_cast<float>(c2[2 - k] * f));
+            sc.fold4[4 - k] = make_float2(static_cast<float>(c4[4 - k] * f), static_cast<float>(c4[4 - k] * f));
+        }
+        sc.limit[0] = fits ? 0.25f / sc.in : -1.f;
+        sc.limit[1] = fits ? 0.5f / sc.in : -1.f;
+        sc.limit[2] = 1.f / sc.in;
+    }
+    return sc;
 }
 inline ScoreParams score_params(const Problem& pr) {
     return score_params(pr.scale, pr.softcap, pr.slopes, pr.slope_sB);
@@ -64,14 +88,9 @@ __device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
 // smallest maximum relative error on its range (exact_tiled_attention_41_b200/fit_tanh_poly.py prints the
 // coefficients; within 5e-7 relative for |x| <= 1/4, 2e-7 up to 1), or the multi-function unit.  A masked score, -inf,
 // stays -inf: the polynomials' leading coefficients are positive.
-// The coefficients stand in constant memory, doubled for the packed FMA.
-#define FA_2(v) {v, v}
-static __constant__ float2 kTanh2[3] = {FA_2(0.12841614f), FA_2(-0.33321908f), FA_2(0.9999996f)};
-static __constant__ float2 kTanh4[5] = {FA_2(0.0171350036f), FA_2(-0.0529860742f), FA_2(0.133247793f),
-                                        FA_2(-0.333330691f), FA_2(1.0f)};
-static __constant__ float2 kTanh6[7] = {FA_2(0.0010410226f), FA_2(-0.00620337902f), FA_2(0.0202899799f),
-                                        FA_2(-0.0534570292f), FA_2(0.13325204f), FA_2(-0.333328396f), FA_2(0.99999994f)};
-#undef FA_2
+static __constant__ float kTanh2[3] = FA_TANH2;
+static __constant__ float kTanh4[5] = FA_TANH4;
+static __constant__ float kTanh6[7] = FA_TANH6;
 enum TanhRange { kTanhQuarter, kTanhHalf, kTanhOne, kTanhAny };
 
 template <int RANGE>
@@ -82,23 +101,42 @@ __device__ __forceinline__ float2 cap_pair(float2 s, float2 in) {
     } else {
         const float2 u = fmul2(x, x);
         constexpr int DEG = RANGE == kTanhQuarter ? 2 : RANGE == kTanhHalf ? 4 : 6;
-        const float2* c = RANGE == kTanhQuarter ? kTanh2 : RANGE == kTanhHalf ? kTanh4 : kTanh6;
-        float2 p = ffma2(c[0], u, c[1]);
+        const float* c = RANGE == kTanhQuarter ? kTanh2 : RANGE == kTanhHalf ? kTanh4 : kTanh6;
+        float2 p = ffma2(splat2(c[0]), u, splat2(c[1]));
 #pragma unroll
-        for (int i = 2; i <= DEG; ++i) p = ffma2(p, u, c[i]);
+        for (int i = 2; i <= DEG; ++i) p = ffma2(p, u, splat2(c[i]));
         return fmul2(p, x);
     }
 }
 
+// out_log2 tanh(in s) + b of a pair of raw scores: the folded polynomials where they reach.
+template <int RANGE>
+__device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc, float2 b) {
+    if constexpr (RANGE == kTanhQuarter || RANGE == kTanhHalf) {
+        const float2 w = fmul2(s, s);
+        float2 p;
+        if constexpr (RANGE == kTanhQuarter) {
+            p = ffma2(ffma2(sc.fold2[0], w, sc.fold2[1]), w, sc.fold2[2]);
+        } else {
+            p = ffma2(sc.fold4[0], w, sc.fold4[1]);
+#pragma unroll
+            for (int i = 2; i < 5; ++i) p = ffma2(p, w, sc.fold4[i]);
+        }
+        return ffma2(s, p, b);
+    } else {
+        return ffma2(cap_pair<RANGE>(s, splat2(sc.in)), splat2(sc.out_log2), b);
+    }
+}
+
 // Calls run(std::integral_constant<int, range>) for the smallest range that holds every argument of the warp
-// (most: the largest |argument| of the thread).  The softmax already keeps the multi-function unit busy with one
+// (most: the largest |raw score| of the thread).  The softmax already keeps the multi-function unit busy with one
 // exponential per score, and a tanh there costs two more results, while the FMA pipe has room; with a cap
 // well above the scores, as caps are chosen, every block of scores takes one of the first ranges.
 template <typename F>
-__device__ __forceinline__ void with_tanh_range(float most, F&& run) {
-    if (__all_sync(0xffffffffu, most <= 0.25f)) run(std::integral_constant<int, kTanhQuarter>{});
-    else if (__all_sync(0xffffffffu, most <= 0.5f)) run(std::integral_constant<int, kTanhHalf>{});
-    else if (__all_sync(0xffffffffu, most <= 1.0f)) run(std::integral_constant<int, kTanhOne>{});
+__device__ __forceinline__ void with_tanh_range(float most, const ScoreParams& sc, F&& run) {
+    if (__all_sync(0xffffffffu, most <= sc.limit[0])) run(std::integral_constant<int, kTanhQuarter>{});
+    else if (__all_sync(0xffffffffu, most <= sc.limit[1])) run(std::integral_constant<int, kTanhHalf>{});
+    else if (__all_sync(0xffffffffu, most <= sc.limit[2])) run(std::integral_constant<int, kTanhOne>{});
     else run(std::integral_constant<int, kTanhAny>{});
 }
 
@@ -112,19 +150,19 @@ __device__ __forceinline__ float max_abs(const float (&s)[N]) {
 
 // s <- tanh(in * s) for a thread's block of raw scores
 template <int N>
-__device__ __forceinline__ void cap_scores(float (&s)[N], float in) {
-    with_tanh_range(max_abs(s) * in, [&](auto range) {
+__device__ __forceinline__ void cap_scores(float (&s)[N], const ScoreParams& sc) {
+    with_tanh_range(max_abs(s), sc, [&](auto range) {
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-            const float2 t = cap_pair<decltype(range)::value>(make_float2(s[e], s[e + 1]), splat2(in));
+            const float2 t = cap_pair<decltype(range)::value>(make_float2(s[e], s[e + 1]), splat2(sc.in));
             s[e] = t.x;
             s[e + 1] = t.y;
         }
     });
 }
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float in) {
-    cap_scores(reinterpret_cast<float (&)[N]>(s), in);
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreParams& sc) {
+    cap_scores(reinterpret_cast<float (&)[N]>(s), sc);
 }
 
 // slope * log2(e) of query head h of sequence b
