@@ -12,6 +12,7 @@ directory; when it is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libfa.so")
@@ -121,11 +122,7 @@ class FAError(RuntimeError):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or x.__class__ is int else x.data_ptr()
 
 
 _current_stream = None
@@ -146,10 +143,15 @@ def _stream(s):
     return s.cuda_stream
 
 
+# workspace sizes depend on the sizes given and nothing else, and asking the library takes 2 us of a call
+_sizes = functools.lru_cache(1024)
+
+
 def status_string(status: int) -> str:
     return load().fa_status_string(int(status)).decode()
 
 
+@_sizes
 def fa_fwd_workspace_size(B, Hq, Hkv, Sq, Sk, D) -> int:
     return load().fa_fwd_workspace_size(B, Hq, Hkv, Sq, Sk, D)
 
@@ -160,6 +162,7 @@ def fa_fwd(q, k, v, out, lse, B, Hq, Hkv, Sq, Sk, D, softmax_scale, causal, work
                          float(softmax_scale), int(bool(causal)), _ptr(workspace), workspace_bytes, _stream(stream))
 
 
+@_sizes
 def fa_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D) -> int:
     return load().fa_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D)
 
@@ -171,6 +174,7 @@ def fa_bwd(q, k, v, out, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, softmax_s
                          workspace_bytes, _stream(stream))
 
 
+@_sizes
 def fa_varlen_fwd_workspace_size(num_seqs, total_q, total_k, Hq, Hkv, D) -> int:
     return load().fa_varlen_fwd_workspace_size(num_seqs, total_q, total_k, Hq, Hkv, D)
 
@@ -183,6 +187,7 @@ def fa_varlen_fwd(q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, max_s
                                 _stream(stream))
 
 
+@_sizes
 def fa_varlen_bwd_workspace_size(num_seqs, total_q, total_k, Hq, Hkv, D) -> int:
     return load().fa_varlen_bwd_workspace_size(num_seqs, total_q, total_k, Hq, Hkv, D)
 
@@ -196,6 +201,7 @@ def fa_varlen_bwd(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_
                                 workspace_bytes, _stream(stream))
 
 
+@_sizes
 def fa_fwd_kvcache_workspace_size(B, Hq, Hkv, Sq, cache_capacity, D, num_splits) -> int:
     return load().fa_fwd_kvcache_workspace_size(B, Hq, Hkv, Sq, cache_capacity, D, num_splits)
 
@@ -241,6 +247,7 @@ def fa_varlen_bwd_ex(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqle
                                    _ptr(workspace), workspace_bytes, _stream(stream))
 
 
+@_sizes
 def fa_fwd_kvcache_ex_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits) -> int:
     return load().fa_fwd_kvcache_ex_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits)
 
@@ -296,6 +303,7 @@ def fa_varlen_bwd_mod(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seql
                                     workspace_bytes, _stream(stream))
 
 
+@_sizes
 def fa_fwd_kvcache_mod_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits,
                                       rotary_dim) -> int:
     return load().fa_fwd_kvcache_mod_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits,

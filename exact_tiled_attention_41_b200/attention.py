@@ -30,6 +30,8 @@ from . import abi
 
 
 def _check(t: torch.Tensor, name: str, dtype=torch.bfloat16):
+    if t.__class__ is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -300,7 +302,7 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
         if t is not None and t.device != x.device:
             raise ValueError(f"{n} must be on the device of x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have the shape and type of x")
     if x.numel() == 0:
