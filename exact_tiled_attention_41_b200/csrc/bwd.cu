@@ -58,6 +58,8 @@ namespace fa {
 // Share of the backward gradient step's exponentials computed on the FMA pipe (exp2_fma2): one pair
 // in kBwdFmaExpEvery, 0 = none.
 constexpr int kBwdFmaExpEvery = FA_BWD_FMA_EXP_EVERY;
+// A cap's tanh takes the FMA pipe itself, so the exponentials stay on the multi-function unit there.
+__host__ __device__ constexpr bool fma_exp_share(int mode) { return kBwdFmaExpEvery > 0 && !(mode & kScoreCap); }
 
 // A dQ accumulator of at most this many bytes (about half of the 126 MB L2) is kept in L2 from the
 // preprocess to the convert with the evict_last policy (the dense prefill workload's is 64 MiB: +1.7 % on
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(512, 1)
                 // they share the exp2 unit; one pair in 6 measured best: +3 % dense, +6 % long-context
                 // GQA, +7 % varlen D = 64 over none, ahead of one in 3 or 4)
                 auto grad = [&](auto poly) {
-                constexpr int kEvery = decltype(poly)::value && !(MODE & kScoreCap) ? kBwdFmaExpEvery : 0;
+                constexpr int kEvery = decltype(poly)::value ? kBwdFmaExpEvery : 0;
                 constexpr int kMod = kEvery > 0 ? kEvery : 1;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 }
                 };
-                if (kBwdFmaExpEvery > 0 && !any_mask && m0 + 128 <= t.Lq) grad(std::true_type{});
+                if (fma_exp_share(MODE) && !any_mask && m0 + 128 <= t.Lq) grad(std::true_type{});
                 else grad(std::false_type{});
                 tmem_st_wait();
                 fence_proxy_async_smem();
@@ -942,7 +944,7 @@ __global__ void __launch_bounds__(384, 1)
                     // the same condition (no masked column in the warp's 64, the whole 128-row query tile inside
                     // the sequence), so both backward modes compute identical P^T and dS^T
                     auto grad = [&](auto poly) {
-                    constexpr int kEvery = decltype(poly)::value && !(MODE & kScoreCap) ? kBwdFmaExpEvery : 0;
+                    constexpr int kEvery = decltype(poly)::value ? kBwdFmaExpEvery : 0;
                     constexpr int kMod = kEvery > 0 ? kEvery : 1;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -986,7 +988,7 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_st16(tmem + lb + C::COL_S(gb) + 32 * half + 16, dd);
                     }
                     };
-                    if (kBwdFmaExpEvery > 0 && !any_mask && row0 - 64 * qh + 128 <= t.Lq) grad(std::true_type{});
+                    if (fma_exp_share(MODE) && !any_mask && row0 - 64 * qh + 128 <= t.Lq) grad(std::true_type{});
                     else grad(std::false_type{});
                     tmem_st_wait();
                     tc_fence_before();
