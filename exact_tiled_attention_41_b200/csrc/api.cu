@@ -128,6 +128,7 @@ static int check_score(float scale, float softcap, const float* slopes, int slop
     if (slopes != nullptr) {
         if (slope_batch_stride != 0 && slope_batch_stride < Hq) return FA_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(slopes) & 3u) return FA_ERR_ALIGNMENT;
+        if (scale < 1e-20f) return FA_ERR_UNSUPPORTED;   // the kernels form slope / scale
     }
     return FA_OK;
 }

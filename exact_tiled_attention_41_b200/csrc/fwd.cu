@@ -224,7 +224,7 @@ __host__ __device__ constexpr bool fixed_reference(int mode) { return (mode & kS
 
 // One tile of a row against its fixed reference: P = exp2(c2 tanh(in s) + bias - reference) for the BK scores at
 // tS, written over them as packed bf16; returns the row's sum.  Columns lo .. hi are allowed (masked: some are
-// not); column c lies at distance d0 - c from the row, and the reference is the bias at distance d_ref.
+// not); column c lies at distance d0 - c from the row; the reference is the bias at distance d_ref and sc.ref_log2.
 template <int BK, int MODE>
 __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& sc, float slope, int d0, int d_ref,
                                                bool past, bool masked, int lo, int hi) {
@@ -254,12 +254,13 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
             across = !behind && !__all_sync(0xffffffffu, dc <= 0);
             step = behind ? slope : -slope;
             base = behind ? -slope * static_cast<float>(dc - d_ref) : slope * static_cast<float>(dc + d_ref);
+            base -= sc.ref_log2;
         }
         uint32_t pk[32];
         auto pairs = [&](auto range, auto bias) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float2 b = (MODE & kScoreBias) ? make_float2(bias(2 * e), bias(2 * e + 1)) : splat2(0.f);
+                const float2 b = (MODE & kScoreBias) ? make_float2(bias(2 * e), bias(2 * e + 1)) : splat2(-sc.ref_log2);
                 const float2 y = cap_pair_log2<decltype(range)::value>(make_float2(x[2 * e], x[2 * e + 1]), sc, b);
                 const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                 if (e & 1) sum1 = fadd2(sum1, pr); else sum0 = fadd2(sum0, pr);
@@ -267,7 +268,7 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
             }
         };
         if (across) {
-            const float from = static_cast<float>(dc), ref = slope * static_cast<float>(d_ref);
+            const float from = static_cast<float>(dc), ref = slope * static_cast<float>(d_ref) - sc.ref_log2;
             pairs(std::integral_constant<int, kTanhAny>{}, [&](int c) { return fmaf(-slope, fabsf(from - c), ref); });
         } else {
             with_tanh_range(most, sc, [&](auto range) {
@@ -285,9 +286,10 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
 // L2: the static deal is balanced there, and the feed's per-unit hand-off measured 2-3 % slower).
 // MODE: score modifiers (score.cuh).
 //  * Capped scores lie within +-cap, so unless the cap is beyond kMaxFixedCap no running maximum is needed: every row is
-//    taken against a fixed reference, the largest bias among its allowed keys (0 without a bias).  The scores
-//    above it are at most cap log2(e) <= 80, and the key with that bias lies at -80 or more: P, the sums and O stay
-//    far inside fp32 and bf16 range, and the result is the same softmax (it does not depend on the reference).
+//    taken against a fixed reference, the largest bias among its allowed keys (0 without a bias) plus
+//    ScoreParams::ref_log2.  The scores above it are then at most 8 to 71 in log2 units, and the key with that bias lies at
+//    -88 or more: P, the sums and O stay inside fp32 and bf16 range, and the result is the same softmax (it
+//    does not depend on the reference).
 //    That leaves one pass over the scores, taken 64 columns at a time from tensor memory, in which the tanh
 //    and exponent arithmetic of the FMA pipe runs beside the exponentials.
 //  * Otherwise (kScoreWide, or a bias alone) the row keeps its reference maximum as without modifiers, and KV tiles are
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                     for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                 }
             }
-            const float ref = FIXED ? -slope * d_ref : m_ref * c2;
+            const float ref = FIXED ? p.sc.ref_log2 - slope * d_ref : m_ref * c2;
             if (valid) *lse_ptr = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             tc_fence_before();
         }

@@ -34,6 +34,9 @@ struct ScoreParams {
     // limit[range]; limit[2]: |in s| <= 1.
     float2 fold2[3], fold4[5];
     float limit[3];
+    // log2 of the factor by which a row's reference lies above its largest bias (the forward's fixed reference): P is at
+    // most 2^8 up to a cap of 33 (as against a running maximum), and at most 2^71 at 55, its least 2^-88
+    float ref_log2;
 };
 
 inline ScoreParams score_params(float scale, float softcap, const float* slopes, int slope_sB) {
@@ -50,6 +53,8 @@ inline ScoreParams score_params(float scale, float softcap, const float* slopes,
         sc.limit[0] = fits ? 0.25f / sc.in : -1.f;
         sc.limit[1] = fits ? 0.5f / sc.in : -1.f;
         sc.limit[2] = 1.f / sc.in;
+        const float top = 2.f * sc.out_log2 - 88.f;
+        sc.ref_log2 = sc.out_log2 - (top > 8.f ? top : 8.f);
     }
     return sc;
 }

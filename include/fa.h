@@ -263,9 +263,10 @@ FA_API int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const 
  *   softcap       0 = no cap; else positive and finite, at most 1e20, with
  *                 1e-20 <= softmax_scale / softcap <= 1e20.
  *   alibi_slopes  DEVICE float32, slope of query head h of sequence b at
- *                 alibi_slopes[b * alibi_batch_stride + h], any finite values; NULL = no
- *                 bias.  alibi_batch_stride is 0 (one set of Hq slopes for all
- *                 sequences) or at least Hq.  Slopes are data: no gradient.
+ *                 alibi_slopes[b * alibi_batch_stride + h], of either sign, magnitude
+ *                 at most 1e10; NULL = no bias.  alibi_batch_stride is 0 (one set of
+ *                 Hq slopes for all sequences) or at least Hq; softmax_scale is then at
+ *                 least 1e-20.  Slopes are data: no gradient.
  * Sk and Sq are the lengths of the sequence (varlen: of each; cache: keys attended to,
  * and Sq).  Distances are formed in float32, exact up to 2^24 tokens.
  * The backward needs the out and lse of the forward with the same modifiers.

@@ -48,6 +48,11 @@ def test_every_call_refuses_bad_modifiers(lib, kw, want):
     assert _kv(**m) == want
 
 
+def test_a_scale_too_small_for_the_bias_is_refused(lib):
+    assert abi.fa_fwd_mod(FAKE, FAKE, FAKE, FAKE, FAKE, 1, 4, 2, 128, 128, 128, 1e-25, 1, -1, -1, 0.0, FAKE, 0,
+                          stream=S0) == abi.FA_ERR_UNSUPPORTED
+
+
 def _kv(**kw):
     a = dict(q=FAKE, k_cache=FAKE, v_cache=FAKE, cache_seqlens=FAKE, k_new=FAKE, v_new=FAKE, seqlen_new=1,
              cache_batch_idx=None, block_table=None, max_blocks_per_seq=0, cache_batch=8, cache_capacity=1024,

@@ -171,6 +171,27 @@ def test_the_cache_call_gives_the_bits_of_the_separate_calls(interleaved, D, rd,
     assert abi.fa_get_device_status() == 0
 
 
+def test_cache_rows_by_index_and_a_full_cache():
+    # cache rows named by cache_batch_idx; a sequence without room keeps its cache and attends to what it holds
+    lens = [5, 64, 63]
+    w = W.kvcache_update(3, 1, 4, 2, 64, 64, lens, seqlen_new=1, seed=2, cache_batch_idx=[4, 0, 2], cache_batch=5)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    cos, sin, _, _ = tables(65, 32)
+    cos, sin = cos.cuda(), sin.cuda()
+    kc, vc = t["k_cache"].clone(), t["v_cache"].clone()
+    out, lse = A.flash_attn_with_kvcache(t["q"], kc, vc, t["cache_seqlens"], w.scale, True, k=t["k_new"], v=t["v_new"],
+                                         cache_batch_idx=t["cache_batch_idx"], rotary_cos=cos, rotary_sin=sin)
+    q = A.apply_rotary(t["q"], cos, sin, t["cache_seqlens"])
+    k = A.apply_rotary(t["k_new"], cos, sin, t["cache_seqlens"])
+    kc2, vc2 = t["k_cache"].clone(), t["v_cache"].clone()
+    out2, lse2 = A.flash_attn_with_kvcache(q, kc2, vc2, t["cache_seqlens"], w.scale, True, k=k, v=t["v_new"],
+                                           cache_batch_idx=t["cache_batch_idx"])
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert torch.equal(kc.view(torch.int16), kc2.view(torch.int16)) and torch.equal(vc.view(torch.int16), vc2.view(torch.int16))
+    assert torch.equal(kc[0].view(torch.int16), t["k_cache"][0].view(torch.int16))     # the full row
+    assert not torch.equal(kc[4, 5], t["k_cache"][4, 5]) and abi.fa_get_device_status() == 0
+
+
 def test_cache_call_reports_positions_past_the_tables():
     w = W.kvcache_update(2, 1, 4, 2, 64, 512, [100, 300], seqlen_new=1, seed=1)
     t = {n: x.cuda() for n, x in w.tensors.items()}
