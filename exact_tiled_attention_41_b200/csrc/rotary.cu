@@ -40,6 +40,12 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, long long tok)
     }
 }
 
+// n / d with a 32-bit division where n allows it: a 64-bit one takes as many instructions as the rest of a row
+__device__ __forceinline__ long long div_small(long long n, int d) {
+    if (n <= 0xffffffffLL) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
+    return n / d;
+}
+
 // A row is one head of one token.  p.items threads share a row: a thread takes the 16-byte piece of four
 // interleaved pairs, the two pieces of eight pairs of halves, or a piece that is only copied.  A block takes
 // consecutive rows (token by token, head by head), kRotRows of them per thread, whose loads are all in flight before
@@ -53,15 +59,22 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     const int slots = kRotThreads / p.items;            // rows side by side
     const int slot = threadIdx.x / p.items, item = threadIdx.x % p.items;
     const long long row0 = static_cast<long long>(blockIdx.x) * (slots * kRotRows);
-    const long long tok0 = row0 / p.H;
+    const long long tok0 = div_small(row0, p.H);
     const int h0 = static_cast<int>(row0 - tok0 * p.H);
     const int half = p.rd / 2;
     const int turned = INTER ? p.rd / 8 : p.rd / 16;    // items of a row that rotate
     const bool turn = item < turned;
     const int d = turn ? item * 8 : p.rd + (item - turned) * 8;
     const int ci = INTER ? d / 2 : d;                   // column of the tables
-    // the sequence of the block's first token; a row's own is at most a few further on
-    const int b0 = p.cu != nullptr ? find_seq(p.cu, p.num_seqs, tok0) : 0;
+    // the sequence and place of the block's first token; a row's own is at most a few further on
+    int b0 = 0;
+    long long pos0 = tok0;
+    if (p.cu != nullptr) {
+        b0 = find_seq(p.cu, p.num_seqs, tok0);
+    } else {
+        b0 = static_cast<int>(div_small(tok0, p.S));
+        pos0 = tok0 - static_cast<long long>(b0) * p.S;
+    }
 
     uint4 u[kRotRows], v[kRotRows];
     const float *cr[kRotRows], *sr[kRotRows];
@@ -88,8 +101,13 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
             xo = tok * p.x_sT;
             yo = tok * p.y_sT;
         } else {
-            b = static_cast<int>(tok / p.S);
-            pos = tok - static_cast<long long>(b) * p.S;
+            b = b0;
+            pos = pos0 + dt;
+            if (pos >= p.S) {
+                const unsigned k_seqs = static_cast<unsigned>(pos) / static_cast<unsigned>(p.S);   // pos < 2^30 + 512
+                b += k_seqs;
+                pos -= static_cast<long long>(k_seqs) * p.S;
+            }
             xo = b * p.x_sB + pos * p.x_sT;
             yo = b * p.y_sB + pos * p.y_sT;
         }
@@ -168,7 +186,9 @@ int launch_rotary(const RotaryCall& c, const Device& dev, cudaStream_t stream) {
 // The angle of row `pos` and pair i is pos * f_i.  An fp32 product would be off by pos * f * 2^-24 radians
 // (0.008 at position 131072), so the angle is formed in turns as an integer: turn_i = f_i / 2 pi as a 64-bit
 // fraction, and pos * turn_i modulo 2^64 is the fraction of a turn, off by at most pos * 2^-53 turns (f_i is
-// a double).  Its upper 32 bits as a signed number are the angle in half turns times 2^31; sincospif does the rest.
+// a double).  Its upper 32 bits give the nearest quarter turn and, as a signed number, what is left: an angle y
+// within pi / 4, exact to 2^-32 turns, whose sine and cosine are polynomials in y^2 (of the smallest maximum
+// relative error; exact_tiled_attention_41_b200/fit_trig_poly.py prints the coefficients).
 struct TableParams {
     uint64_t turn[128];   // rd / 2 <= 128 pairs
     float* cos;
@@ -176,6 +196,24 @@ struct TableParams {
     int rows, half;
     float amplitude;
 };
+
+// sine and cosine of a fraction of a turn
+__device__ __forceinline__ void sin_cos_turn(uint32_t frac, float& sn, float& cs) {
+    const uint32_t quarter = (frac + 0x20000000u) >> 30;
+    const float y = static_cast<float>(static_cast<int32_t>(frac - (quarter << 30))) * 1.4629180792671596e-9f;   // 2 pi 2^-32
+    const float u = y * y;
+    float s = fmaf(-0.00019501822f, u, 0.00833201688f);
+    s = fmaf(s, u, -0.166666508f);
+    s = fmaf(s, u, 1.0f) * y;
+    float c = fmaf(2.4372679e-05f, u, -0.00138865295f);
+    c = fmaf(c, u, 0.041666612f);
+    c = fmaf(c, u, -0.5f);
+    c = fmaf(c, u, 1.0f);
+    // a quarter turn takes (cos, sin) to (-sin, cos)
+    const bool odd = quarter & 1;
+    sn = __uint_as_float(__float_as_uint(odd ? c : s) ^ ((quarter & 2) << 30));
+    cs = __uint_as_float(__float_as_uint(odd ? s : c) ^ (((quarter + 1) & 2) << 30));
+}
 
 // A thread owns four neighbouring pairs of a column block and walks down the rows: one 16-byte store to each table
 // per row, and the frequencies stay in registers.
@@ -199,7 +237,7 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant
         float s[4], c[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            sincospif(static_cast<float>(static_cast<int32_t>(frac[e] >> 32)) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31
+            sin_cos_turn(static_cast<uint32_t>(frac[e] >> 32), s[e], c[e]);
             frac[e] += step[e];
         }
         const float a = p.amplitude;

@@ -109,7 +109,7 @@ def test_tables(rows, rd, scaling):
     cos, sin = A.rotary_tables(rows, rd, 50000.0, scaling, original_seqlen=2048, low_rotations=1.0, high_rotations=20.0, **kw)
     c, s = M.rotary_tables(rows, rd, 50000.0, scaling, original=2048, low=1.0, high=20.0, **kw)
     assert cos.shape == (rows, rd // 2) and cos.is_contiguous() and sin.is_contiguous()
-    # fp32 angle in half turns: 2^-25 absolute (times pi), sincospi 2 ulp, one product
+    # the angle to 2^-25 of a half turn (times pi), sine and cosine to 3 half steps of fp32 at 1, one product
     for got, want in ((cos, c), (sin, s)):
         assert np.abs(f64(got) - want).max() <= 1.2 * (np.pi * 2.0 ** -25 + 3 * 2.0 ** -24)
 
