@@ -156,6 +156,28 @@ def test_steep_slopes_over_a_long_context():
         check_dense(w, NONE, 0.0, torch.tensor([8.0, -0.05]), causal=causal)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("det", [False, True])
+@pytest.mark.parametrize("Sq,Sk,window,softcap,kind", [(150, 150, (1, 0), 20.0, None), (90, 400, (2, 1), 0.0, "falling"),
+                                                       (2, 300, NONE, 30.0, "falling"), (40, 40, NONE, 0.0, "mixed")])
+def test_gradients_of_rows_with_few_keys(D, det, Sq, Sk, window, softcap, kind):
+    # Rounding to bf16 is off by 2^-8 / sqrt(3) / m for a mantissa m in [1, 2), 1.6e-3 of the value on average.  dS, the
+    # products' result and the stored gradient make three of them at most: 2.8e-3 of the norm, 4e-3 with room for a sample
+    # of a few rows.  Delta from the rounded output alone would add 5e-3 here.
+    w = W.dense(3, Sq, Sk, 4, 2, D, True, seed=D + Sq)
+    w.tensors["q"].mul_(2)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    slopes = None if kind is None else slopes_of(4, kind=kind)
+    sl = None if slopes is None else slopes.cuda()
+    out, lse = A.flash_attn_func(t["q"], t["k"], t["v"], w.scale, True, window, softcap, sl)
+    grads = A.flash_attn_backward(t["do"], t["q"], t["k"], t["v"], out, lse, w.scale, True, window, det, softcap, sl)
+    ref = M.attention(*(f64(w.tensors[n]) for n in ("q", "k", "v")), w.scale, True, window, softcap,
+                      None if slopes is None else slopes.numpy(), f64(w.tensors["do"]))
+    for name, x in zip(("dq", "dk", "dv"), grads):
+        want = np.stack([r[name] for r in ref])
+        assert np.linalg.norm(f64(x) - want) <= 4e-3 * np.linalg.norm(want), name
+
+
 def test_captured_replayed_and_on_another_stream():
     w = W.dense(2, 200, 200, 4, 2, 128, True, seed=5)
     t = {n: x.cuda() for n, x in w.tensors.items()}
