@@ -192,6 +192,8 @@ def flash_attn_with_kvcache(q, k_cache, v_cache, cache_seqlens, softmax_scale=No
         _check(k, "k")
         _check(v, "v")
         sn = k.shape[1]
+        if k.shape != v.shape or k.shape != (B, sn, k_cache.shape[2], D):
+            raise ValueError(f"k and v must be (B, seqlen_new, Hkv, D), got {tuple(k.shape)} and {tuple(v.shape)}")
     if cache_batch_idx is not None:
         _check(cache_batch_idx, "cache_batch_idx", torch.int32)
     max_blocks = 0
@@ -272,7 +274,7 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
     the other strides multiples of 8 (a slice of a packed projection will do).  cos, sin (seqlen_ro, rotary_dim / 2)
     float32.  A token's position is its index in its sequence plus seqlen_offsets (an int, or int32 (B,)).
     Pairs are adjacent values (interleaved) or values rotary_dim / 2 apart.  inverse rotates by the opposite angle,
-    which is the gradient.  out may be x (in place).  Returns out, contiguous unless given.  Rows of out behind the
+    which is the gradient (RotaryFunction records it for autograd; this call does not).  out may be x (in place).  Returns out, contiguous unless given.  Rows of out behind the
     last sequence of a packed batch are not written.
     """
     if not isinstance(x, torch.Tensor):

@@ -241,6 +241,8 @@ def test_refusals():
         A.flash_attn_with_kvcache(q, cache, cache.clone(), 3, rotary_cos=cos, rotary_sin=cos)
     with pytest.raises(ValueError):
         A.flash_attn_with_kvcache(q, cache, cache.clone(), 3, k=q, v=q, rotary_cos=cos)
+    with pytest.raises(ValueError):       # new keys of another head count
+        A.flash_attn_with_kvcache(q, cache, cache.clone(), 3, k=q[:, :, :1].contiguous(), v=q[:, :, :1].contiguous())
 
 
 def test_training_step_through_rotary_and_capped_attention():

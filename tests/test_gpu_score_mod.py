@@ -87,7 +87,7 @@ def test_scores_far_beyond_the_cap_and_around_every_tanh_branch():
     check_dense(w, NONE, 1.0, None, det=True)
 
 
-@pytest.mark.parametrize("softcap", [20.0, 33.5, 50.0, 55.0, 56.0, 300.0])
+@pytest.mark.parametrize("softcap", [1e-6, 0.01, 20.0, 33.5, 50.0, 55.0, 56.0, 300.0])
 @pytest.mark.parametrize("slope", [None, 0.7, -0.7])
 def test_saturated_scores_on_both_sides_of_the_widest_fixed_reference(softcap, slope):
     # one key vector for all keys: rows of +c u score +cap with every key, rows of -c u score -cap, whole rows of either
@@ -97,7 +97,7 @@ def test_saturated_scores_on_both_sides_of_the_widest_fixed_reference(softcap, s
     w.tensors["k"][0, :, 0] = u
     w.tensors["k"][0, 1::7, 0] = -u
     for i in range(190):
-        w.tensors["q"][0, i, 0] = u * (-1) ** (i // 3) * (softcap if i % 2 else 0.02 * softcap)
+        w.tensors["q"][0, i, 0] = u * (-1) ** (i // 3) * max(softcap, 1.0) * (1.0 if i % 2 else 0.02)
     w.tensors["v"].mul_(1e4)
     check_dense(w, NONE, softcap, None if slope is None else torch.tensor([slope]), det=True)
 
