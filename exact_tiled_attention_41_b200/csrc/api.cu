@@ -467,13 +467,25 @@ static KvCall plain_kv_call(const void* q, const void* k_cache, const void* v_ca
     return c;
 }
 
-static int run_kv_call(const KvCall& c, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+// Bytes that cover the automatic split of the call with score modifiers and without.
+static size_t kv_bytes_either(KvCall c) {
+    c.softcap = 0.f;
+    c.slopes = nullptr;
+    const size_t without = kvcache_workspace_bytes(c, kvcache_chunk(c, 148));
+    c.softcap = 1.f;   // only its presence matters for the split
+    const size_t with = kvcache_workspace_bytes(c, kvcache_chunk(c, 148));
+    return with > without ? with : without;
+}
+
+// either: the workspace must have the size that covers both splits (fa_fwd_kvcache_mod)
+static int run_kv_call(const KvCall& c, void* workspace, size_t workspace_bytes, fa_stream_t stream,
+                       bool either = false) {
     int st = kvcache_validate(c, true);
     if (st != FA_OK) return st;
     if (!workspace) return FA_ERR_INVALID_ARG;
     if (!aligned256(workspace)) return FA_ERR_ALIGNMENT;
     const int chunk = kvcache_chunk(c, 148);
-    if (workspace_bytes < kvcache_workspace_bytes(c, chunk)) return FA_ERR_WORKSPACE;
+    if (workspace_bytes < (either ? kv_bytes_either(c) : kvcache_workspace_bytes(c, chunk))) return FA_ERR_WORKSPACE;
     Device dev;
     if (get_device(&dev) != FA_OK) return FA_ERR_CUDA;
     return kvcache_launch(c, chunk, workspace, dev, static_cast<cudaStream_t>(stream));
@@ -495,7 +507,7 @@ int fa_fwd_kvcache(const void* q, const void* k_cache, const void* v_cache, cons
 }
 
 static size_t kv_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity, int max_blocks_per_seq,
-                                int num_splits, int rotary_dim) {
+                                int num_splits, int rotary_dim, bool either) {
     KvCall c = plain_kv_call(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hq, Hkv, Sq, cache_capacity, D,
                              1.0f, 0, num_splits);
     if (max_blocks_per_seq < 0) return 0;
@@ -506,12 +518,12 @@ static size_t kv_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache
     }
     c.rotary_dim = rotary_dim;
     if (kvcache_validate(c, false) != FA_OK) return 0;
-    return kvcache_workspace_bytes(c, kvcache_chunk(c, 148));
+    return either ? kv_bytes_either(c) : kvcache_workspace_bytes(c, kvcache_chunk(c, 148));
 }
 
 size_t fa_fwd_kvcache_ex_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
                                         int max_blocks_per_seq, int num_splits) {
-    return kv_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits, 0);
+    return kv_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits, 0, false);
 }
 
 int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const int32_t* cache_seqlens, const void* k_new,
@@ -519,15 +531,23 @@ int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const int32_t
                       int max_blocks_per_seq, int cache_batch, int cache_capacity, void* out, float* lse, int B,
                       int Hq, int Hkv, int Sq, int D, float softmax_scale, int causal, int window_left,
                       int window_right, int num_splits, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
-    return fa_fwd_kvcache_mod(q, k_cache, v_cache, cache_seqlens, k_new, v_new, seqlen_new, cache_batch_idx,
-                              block_table, max_blocks_per_seq, cache_batch, cache_capacity, out, lse, B, Hq, Hkv, Sq, D,
-                              softmax_scale, causal, window_left, window_right, num_splits, 0.f, nullptr, 0, nullptr,
-                              nullptr, 0, 0, 0, workspace, workspace_bytes, stream);
+    KvCall c = plain_kv_call(q, k_cache, v_cache, cache_seqlens, out, lse, B, Hq, Hkv, Sq, cache_capacity, D,
+                             softmax_scale, causal, num_splits);
+    c.k_new = k_new;
+    c.v_new = v_new;
+    c.seqlen_new = seqlen_new;
+    c.cache_batch_idx = cache_batch_idx;
+    c.block_table = block_table;
+    c.max_blocks_per_seq = max_blocks_per_seq;
+    c.cache_batch = cache_batch;
+    c.window_left = window_left;
+    c.window_right = window_right;
+    return run_kv_call(c, workspace, workspace_bytes, stream);
 }
 
 size_t fa_fwd_kvcache_mod_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
                                          int max_blocks_per_seq, int num_splits, int rotary_dim) {
-    return kv_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits, rotary_dim);
+    return kv_workspace_size(B, Hq, Hkv, Sq, D, cache_capacity, max_blocks_per_seq, num_splits, rotary_dim, true);
 }
 
 int fa_fwd_kvcache_mod(const void* q, void* k_cache, void* v_cache, const int32_t* cache_seqlens, const void* k_new,
@@ -559,7 +579,7 @@ int fa_fwd_kvcache_mod(const void* q, void* k_cache, void* v_cache, const int32_
     c.rotary_len = rotary_len;
     c.rotary_dim = rotary_dim;
     c.rotary_interleaved = rotary_interleaved;
-    return run_kv_call(c, workspace, workspace_bytes, stream);
+    return run_kv_call(c, workspace, workspace_bytes, stream, true);
 }
 
 // ----------------------------------------------------------------------- rotary positions

@@ -624,6 +624,16 @@ int kvcache_chunk(const KvCall& c, int num_sms) {
     long long ch;
     if (c.num_splits > 0) {
         ch = (static_cast<long long>(cap) + c.num_splits - 1) / c.num_splits;
+    } else if (score_mode(c.softcap, c.slopes) != kScorePlain) {
+        // about 2.5 waves of resident split CTAs, assuming caches half full on average (the whole call, B200: 32 x 8
+        // heads of 1-8K keys, D = 128: 14 splits, 6 waves, 124 us, 5 splits 119.5; 16 x 16 heads of 512-2052 keys,
+        // D = 256, one CTA per SM: 5 splits 85 us, 3 splits 77).  At least 512 keys a split, or 256 where 512 would
+        // leave SMs idle (one sequence of 1235 keys, 4 heads: 14.5 us with 512, 12.1 with 256).  Calls without
+        // modifiers keep the split, and the bits, that they had.
+        const long long resident = static_cast<long long>(num_sms) * (c.D == 256 ? 1 : 2);
+        ch = parallel * cap / (5 * resident);
+        const long long least = parallel * ((cap + 511) / 512) < resident ? 256 : 512;
+        if (ch < least) ch = least;
     } else {
         // aim for about 6 waves of split CTAs (2 per SM), assuming caches half full on average, with at
         // least 512 keys per split: shorter splits spend a large share of their time starting up (B200, 64

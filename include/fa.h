@@ -313,6 +313,8 @@ FA_API int fa_varlen_bwd_mod(const void* q, const void* k, const void* v, const 
  * a multiple of 16, at most D; rotary_interleaved as for fa_rotary.  A position at or
  * past rotary_len records FA_ERR_INVALID_ARG in the device status word, and the row
  * becomes zeros.  rotary_dim = 0 with NULL tables: no rotary.
+ * With a cap or a bias the automatic split (num_splits = 0) is another one than without;
+ * the workspace size covers both.
  */
 FA_API size_t fa_fwd_kvcache_mod_workspace_size(int B, int Hq, int Hkv, int Sq, int D, int cache_capacity,
                                                 int max_blocks_per_seq, int num_splits, int rotary_dim);
