@@ -93,7 +93,7 @@ _SIGS = {
     "fa_fwd_kvcache_mod_workspace_size": (_Z, [_I] * 9),
     "fa_fwd_kvcache_mod": (_I, [_P] * 6 + [_I] + [_P] * 2 + [_I] * 3 + [_P] * 2 + [_I] * 5 + [_F] + [_I] * 4
                            + [_F, _P, _I, _P, _P, _I, _I, _I] + [_P, _Z, _P]),
-    "fa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_I64] * 6 + [_I, _I, _P]),
+    "fa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_I64] * 6 + [_I, _I, _I, _P]),
     "fa_rotary_tables": (_I, [_P, _P, _I, _I, _D, _I, _D, _I, _D, _D, _D, _P]),
 }
 
@@ -327,11 +327,11 @@ def fa_fwd_kvcache_mod(q, k_cache, v_cache, cache_seqlens, k_new, v_new, seqlen_
 
 def fa_rotary(x, y, rotary_cos, rotary_sin, cu_seqlens, seqlen_offsets, seqlen_offset, num_seqs, S, total, H, D,
               rotary_dim, rotary_len, x_stride_seq, x_stride_tok, x_stride_head, y_stride_seq, y_stride_tok,
-              y_stride_head, interleaved, inverse, stream=None) -> int:
+              y_stride_head, interleaved, inverse, zero_tail=False, stream=None) -> int:
     return load().fa_rotary(_ptr(x), _ptr(y), _ptr(rotary_cos), _ptr(rotary_sin), _ptr(cu_seqlens),
                             _ptr(seqlen_offsets), int(seqlen_offset), num_seqs, S, total, H, D, rotary_dim, rotary_len,
                             x_stride_seq, x_stride_tok, x_stride_head, y_stride_seq, y_stride_tok, y_stride_head,
-                            int(bool(interleaved)), int(bool(inverse)), _stream(stream))
+                            int(bool(interleaved)), int(bool(inverse)), int(bool(zero_tail)), _stream(stream))
 
 
 def fa_rotary_tables(rotary_cos, rotary_sin, rotary_len, rotary_dim, base, scaling, factor, original_len,

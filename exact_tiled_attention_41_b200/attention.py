@@ -25,6 +25,7 @@ import functools
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import abi
 
@@ -274,8 +275,9 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
     the other strides multiples of 8 (a slice of a packed projection will do).  cos, sin (seqlen_ro, rotary_dim / 2)
     float32.  A token's position is its index in its sequence plus seqlen_offsets (an int, or int32 (B,)).
     Pairs are adjacent values (interleaved) or values rotary_dim / 2 apart.  inverse rotates by the opposite angle,
-    which is the gradient (RotaryFunction records it for autograd; this call does not).  out may be x (in place).  Returns out, contiguous unless given.  Rows of out behind the
-    last sequence of a packed batch are not written.
+    which is the gradient (RotaryFunction records it for autograd; this call does not).  out may be x (in place);
+    other overlaps are not supported.  Returns out, contiguous unless given.  Rows behind the last sequence of a
+    packed batch are zeros in a new out and are not written in a given one.
     """
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
@@ -303,14 +305,15 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
     for t, n in ((offsets, "seqlen_offsets"), (cu_seqlens, "cu_seqlens"), (out, "out")):
         if t is not None and t.device != x.device:
             raise ValueError(f"{n} must be on the device of x")
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have the shape and type of x")
     if x.numel() == 0:
         return out
     _raise(abi.fa_rotary(x, out, cos, sin, cu_seqlens, offsets, seqlen_offsets, B, S, total, H, D, rd, rows,
-                         *_rotary_strides(x, "x"), *_rotary_strides(out, "out"), interleaved, inverse), "fa_rotary")
+                         *_rotary_strides(x, "x"), *_rotary_strides(out, "out"), interleaved, inverse, new), "fa_rotary")
     return out
 
 
@@ -357,7 +360,7 @@ class FlashAttnFunction(torch.autograd.Function):
 
 
 class RotaryFunction(torch.autograd.Function):
-    """Autograd wrapper of apply_rotary; the gradient is the rotation by the opposite angle."""
+    """Autograd wrapper of apply_rotary; the gradient is the rotation by the opposite angle (first order only)."""
 
     @staticmethod
     def forward(ctx, x, cos, sin, seqlen_offsets=0, interleaved=True, cu_seqlens=None):
@@ -369,6 +372,7 @@ class RotaryFunction(torch.autograd.Function):
         return apply_rotary(x, cos, sin, seqlen_offsets, interleaved, False, cu_seqlens)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         cos, sin, offsets, cu_seqlens = ctx.saved_tensors
         dx = apply_rotary(dy.contiguous(), cos, sin, ctx.offset if offsets is None else offsets, ctx.interleaved, True,

@@ -587,7 +587,7 @@ int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rota
               const int32_t* seqlen_offsets, int seqlen_offset, int num_seqs, int S, int total, int H, int D,
               int rotary_dim, int rotary_len, long long x_stride_seq, long long x_stride_tok, long long x_stride_head,
               long long y_stride_seq, long long y_stride_tok, long long y_stride_head, int interleaved, int inverse,
-              fa_stream_t stream) {
+              int zero_tail, fa_stream_t stream) {
     if (!x || !y || !rotary_cos || !rotary_sin) return FA_ERR_INVALID_ARG;
     if (num_seqs <= 0 || H <= 0 || D <= 0 || rotary_len <= 0 || seqlen_offset < 0) return FA_ERR_INVALID_ARG;
     if (cu_seqlens != nullptr ? total <= 0 : S <= 0) return FA_ERR_INVALID_ARG;
@@ -612,6 +612,7 @@ int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rota
     const long long len = cu_seqlens != nullptr ? total : S;
     if ((H > 1 && ys[2] < D) || (len > 1 && ys[1] < D) || (cu_seqlens == nullptr && num_seqs > 1 && ys[0] < D))
         return FA_ERR_INVALID_ARG;
+    if (x == y && zero_tail) return FA_ERR_INVALID_ARG;
     if (x == y && (xs[1] != ys[1] || xs[2] != ys[2] || (cu_seqlens == nullptr && xs[0] != ys[0])))
         return FA_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(y) || !aligned16(rotary_cos) || !aligned16(rotary_sin)) return FA_ERR_ALIGNMENT;
@@ -634,6 +635,7 @@ int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rota
     c.seqlen_ro = rotary_len;
     c.interleaved = interleaved != 0;
     c.inverse = inverse != 0;
+    c.zero_tail = zero_tail;
     return launch_rotary(c, dev, static_cast<cudaStream_t>(stream));
 }
 

@@ -133,7 +133,7 @@ struct RotaryCall {
     const float* sin;
     const int32_t* cu_seqlens;       // device [num_seqs + 1] or NULL
     const int32_t* offsets;          // device [num_seqs] or NULL
-    int offset, num_seqs, S, H, D, rotary_dim, seqlen_ro, interleaved, inverse;
+    int offset, num_seqs, S, H, D, rotary_dim, seqlen_ro, interleaved, inverse, zero_tail;
     long long tokens;
     long long x_stride[3], y_stride[3];   // sequence, token, head
 };

@@ -20,6 +20,7 @@ struct RotaryParams {
     long long tokens;
     long long x_sB, x_sT, x_sH, y_sB, y_sT, y_sH;   // strides in values; sB unused with cu
     int inverse;
+    int zero_tail;            // rows of y outside every sequence of a packed batch: zeros, or left as they were
     int items;                // threads per row: pieces (interleaved) or pairs of pieces (halves), and copied pieces
     int* status;
 };
@@ -95,8 +96,13 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         if (p.cu != nullptr) {
             b = b0;
             while (b < p.num_seqs && __ldg(p.cu + b + 1) <= tok) ++b;
-            if (b < 0 || b >= p.num_seqs) {              // behind the last sequence: left as it was
+            if (b < 0 || b >= p.num_seqs) {              // outside every sequence
                 live[k] = false;
+                if (p.zero_tail) {
+                    __nv_bfloat16* z = p.y + tok * p.y_sT + h * p.y_sH + d;
+                    *reinterpret_cast<uint4*>(z) = make_uint4(0, 0, 0, 0);
+                    if (!INTER && turn) *reinterpret_cast<uint4*>(z + half) = make_uint4(0, 0, 0, 0);
+                }
                 continue;
             }
             pos = tok - __ldg(p.cu + b);
@@ -171,6 +177,7 @@ int launch_rotary(const RotaryCall& c, const Device& dev, cudaStream_t stream) {
     p.y_sT = c.y_stride[1];
     p.y_sH = c.y_stride[2];
     p.inverse = c.inverse;
+    p.zero_tail = c.zero_tail;
     p.items = (c.interleaved ? c.rotary_dim / 8 : c.rotary_dim / 16) + (c.x != c.y ? (c.D - c.rotary_dim) / 8 : 0);
     p.status = dev.status;
     const long long per_block = kRotThreads / p.items * kRotRows;

@@ -345,15 +345,16 @@ FA_API int fa_fwd_kvcache_mod(const void* q, void* k_cache, void* v_cache, const
  *   rotary_cos, rotary_sin  float32 [rotary_len][rotary_dim / 2], 16-byte aligned;
  *         rotary_dim a multiple of 16, at most D.
  * A position outside the tables records FA_ERR_INVALID_ARG in the device status word, and
- * the rotated values of the row become zeros.  Rows of y behind the last sequence of a packed
- * batch are left as they are.  No workspace.
+ * the rotated values of the row become zeros.  Rows of y outside every sequence of a packed
+ * batch (behind the last one) are left as they are, or with zero_tail != 0 (not in place)
+ * become zeros, which is their gradient.  No workspace.
  */
 FA_API int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rotary_sin,
                      const int32_t* cu_seqlens, const int32_t* seqlen_offsets, int seqlen_offset,
                      int num_seqs, int S, int total, int H, int D, int rotary_dim, int rotary_len,
                      long long x_stride_seq, long long x_stride_tok, long long x_stride_head,
                      long long y_stride_seq, long long y_stride_tok, long long y_stride_head,
-                     int interleaved, int inverse, fa_stream_t stream);
+                     int interleaved, int inverse, int zero_tail, fa_stream_t stream);
 
 /* fa_rotary_tables: row p, column i of the tables is amplitude * cos / sin (p * f_i),
  * i < rotary_dim / 2, p < rotary_len, with f_i = base^(-2i / rotary_dim) scaled for contexts

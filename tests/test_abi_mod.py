@@ -125,6 +125,10 @@ def test_rotary_refuses_bad_arguments(lib, kw, want):
     assert _rotary(**kw) == want
 
 
+def test_rotary_in_place_refuses_a_zeroed_tail(lib):
+    assert _rotary(cu_seqlens=FAKE, total=8, y=FAKE, zero_tail=1) == abi.FA_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("kw,want", [
     (dict(rotary_cos=None), abi.FA_ERR_INVALID_ARG),
     (dict(rotary_len=0), abi.FA_ERR_INVALID_ARG),

@@ -314,3 +314,33 @@ def test_captured_cache_call_replays_at_the_next_length():
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wl) and torch.equal(ka, kc) and torch.equal(va, vc)
         lens += 1
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("rd", [64, 32])
+def test_padding_of_a_packed_batch_gets_zeros_in_new_tensors(interleaved, rd):
+    """Rows behind the last sequence (and before the first) are zeros in a new output and in the gradient, whatever
+    the memory held."""
+    cos, sin, c, s = tables(40, rd)
+    cu = torch.tensor([2, 30, 30, 41], dtype=torch.int32).cuda()
+    x = normal(21, 60, 3, 64).cuda().requires_grad_()
+    pos = np.concatenate([np.arange(28), np.arange(11)])
+    dy = normal(22, 60, 3, 64)
+    dy[41:] = float("nan")
+    dy = dy.cuda()
+    poison = [torch.full_like(x, float("nan"), requires_grad=False) for _ in range(4)]
+    del poison                                        # the next tensors of this size lie there
+    y = A.RotaryFunction.apply(x, cos.cuda(), sin.cuda(), 0, interleaved, cu)
+    g, = torch.autograd.grad(y, x, dy)
+    for t, src, inverse in ((y.detach(), x.detach(), False), (g, dy, True)):
+        assert (t[:2] == 0).all() and (t[41:] == 0).all()
+        check(t[2:41], f64(src)[2:41], c, s, pos, interleaved, inverse=inverse)
+
+
+def test_rotary_gradient_is_first_order():
+    cos, sin, _, _ = tables(8, 32)
+    x = normal(23, 1, 4, 2, 64).cuda().requires_grad_()
+    y = A.RotaryFunction.apply(x, cos.cuda(), sin.cuda())
+    g, = torch.autograd.grad(y, x, torch.ones_like(y, requires_grad=True), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
