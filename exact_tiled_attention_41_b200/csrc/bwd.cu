@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(512, 1)
     // p_full / p_full_hi: compute warpgroup 0 (query columns 0-63) / 1 (64-127) done
     const uint32_t s_full = b0 + 8u * (2 + 2 * ST), p_full = s_full + 8, dq_full = s_full + 16,
                    dq_empty = s_full + 24, dkv_full = s_full + 32, dq_empty_hi = s_full + 40, p_full_hi = s_full + 48,
-                   v_full = s_full + 56, v_free = s_full + 64, dv_done = s_full + 72;
+                   v_full = s_full + 56, v_free = s_full + 64, dv_done = s_full + 72, raw = b0 + 8u * (C::NUM_BARS + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int PRODUCER = 12, MMA = 13, MMA_B = 14;
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(bars + 2 + 2 * ST + 10 + s, 1);                            // unit published
             mbar_init(bars + 2 + 2 * ST + 10 + kFeedSlots + s, DQ ? 14 : 10);    // read by the issuers, compute (, dQ) warps
         }
+        mbar_init(bars + C::NUM_BARS + 1, 1);   // raw: a tile that ends past its sequence has arrived
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(512, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
         if (warp == PRODUCER) {
             // -------------------------------------------------------- producer (whole warp)
-            uint32_t unit_it = 0, q_it = 0;
+            uint32_t unit_it = 0, q_it = 0, raw_it = 0;
             bool ok = true;
             for (uint32_t fi = 0; ok; ++fi) {
                 int u = 0;
@@ -287,38 +288,55 @@ __global__ void __launch_bounds__(512, 1)
                         sLSE[st * 128 + qi] = in ? -__ldg(p.lse2 + idx) : -INFINITY;
                         sDel[st * 128 + qi] = in ? -__ldg(p.delta + idx) : 0.f;
                     }
+                    // with score modifiers, rows past the sequence become zeros before the products read them
+                    const bool past = MODE != kScorePlain && m0 + 128 > t.Lq;
+                    const uint32_t bar = past ? raw : q_full(st);
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(q_full(st), 2 * C::T_BYTES);
+                        mbar_arrive_expect_tx(bar, 2 * C::T_BYTES);
 #pragma unroll
                         for (int c = 0; c < C::NCHUNK; ++c) {
-                            tma_load_3d(smem_u32(smem + C::OFF_Q + st * C::T_BYTES + c * 128 * 128), &tmQ, q_full(st),
+                            tma_load_3d(smem_u32(smem + C::OFF_Q + st * C::T_BYTES + c * 128 * 128), &tmQ, bar,
                                         c * 64, h, t.q_start + m0);
                             tma_load_3d(smem_u32(smem + C::OFF_DO + st * C::T_BYTES + c * 128 * 128), &tmDO,
-                                        q_full(st), c * 64, h, t.q_start + m0);
+                                        bar, c * 64, h, t.q_start + m0);
                         }
+                    }
+                    if (past) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) return false;
+                        zero_rows<C::NCHUNK, 128, 32>(smem + C::OFF_Q + st * C::T_BYTES, t.Lq - m0, lane);
+                        zero_rows<C::NCHUNK, 128, 32>(smem + C::OFF_DO + st * C::T_BYTES, t.Lq - m0, lane);
+                        fence_proxy_async_smem();
+                        if (lane == 0) mbar_arrive(q_full(st));   // in place of the loads' expect-tx
                     }
                     mbar_arrive(q_full(st));
                     ++q_it;
                     return true;
                 };
+                // the unit's K or V tile; a tile that ends past the sequence is cleaned as Q and dO are
+                auto load_kv = [&](uint32_t off, const CUtensorMap* map, uint32_t full) -> bool {
+                    const bool past = MODE != kScorePlain && t.n0 + 128 > t.Lk;
+                    const uint32_t bar = past ? raw : full;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, C::T_BYTES);
+#pragma unroll
+                        for (int c = 0; c < C::NCHUNK; ++c)
+                            tma_load_3d(smem_u32(smem + off + c * 128 * 128), map, bar, c * 64, t.hk, t.k_start + t.n0);
+                    }
+                    if (past) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) return false;
+                        zero_rows<C::NCHUNK, 128, 32>(smem + off, t.Lk - t.n0, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full);
+                    }
+                    return true;
+                };
                 // V (free once the previous unit's last dP^T has run), the first Q / dO tile, then K
                 if (unit_it > 0 && !mbar_wait(v_free, (unit_it - 1) & 1, w)) { ok = false; break; }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(v_full, C::T_BYTES);
-#pragma unroll
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_3d(smem_u32(smem + C::OFF_V + c * 128 * 128), &tmV, v_full, c * 64, t.hk,
-                                    t.k_start + t.n0);
-                }
+                if (!load_kv(C::OFF_V, &tmV, v_full)) { ok = false; break; }
                 if (!load_tile(0)) { ok = false; break; }
                 if (unit_it > 0 && !mbar_wait(k_free, (unit_it - 1) & 1, w)) { ok = false; break; }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(k_full, C::T_BYTES);
-#pragma unroll
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_3d(smem_u32(smem + C::OFF_K + c * 128 * 128), &tmK, k_full, c * 64, t.hk,
-                                    t.k_start + t.n0);
-                }
+                if (!load_kv(C::OFF_K, &tmK, k_full)) { ok = false; break; }
                 ++unit_it;
                 for (int it = 1; it < t.n_it && ok; ++it)
                     if (!load_tile(it)) ok = false;
@@ -728,7 +746,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t bb = b0 + 8u * (2 + 2 * ST);
     auto s_full = [&](int b) { return bb + 8u * b; };
     auto p_full = [&](int b) { return bb + 16 + 8u * b; };
-    const uint32_t dkv_full = bb + 32, dkv_empty = bb + 40;
+    const uint32_t dkv_full = bb + 32, dkv_empty = bb + 40, raw = b0 + 8u * (C::NUM_BARS + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int PRODUCER = 8, MMA = 9;
@@ -750,6 +768,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         mbar_init(bars + 2 + 2 * ST + 4, 1);            // dkv_full
         mbar_init(bars + 2 + 2 * ST + 5, 256);          // dkv_empty: both epilogues read dV / dK
+        mbar_init(bars + C::NUM_BARS + 1, 1);   // raw: a tile that ends past its sequence has arrived
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -774,22 +793,33 @@ __global__ void __launch_bounds__(384, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
         if (warp == PRODUCER) {
             // -------------------------------------------------------- producer (whole warp)
-            uint32_t unit_it = 0, q_it = 0;
+            uint32_t unit_it = 0, q_it = 0, raw_it = 0;
             bool ok = true;
             for (int k = 0, u = snake_unit(0, p.num_units); u >= 0 && ok; u = snake_unit(++k, p.num_units)) {
                 if (u >= p.num_units) continue;
                 const BUnit t = decode_bunit(p, u);
                 if (t.skip || t.n_it == 0) continue;
                 if (unit_it > 0 && !mbar_wait(kv_empty, (unit_it - 1) & 1, w)) { ok = false; break; }
+                // tiles that end past their sequence are cleaned as in bwd_kernel
+                const bool k_past = MODE != kScorePlain && t.n0 + 128 > t.Lk;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(kv_full, 2 * C::KV_BYTES);
+                    const uint32_t bar = k_past ? raw : kv_full;
+                    mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES);
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
-                        tma_load_3d(smem_u32(smem + C::OFF_K + c * 128 * 128), &tmK, kv_full, c * 64, t.hk,
+                        tma_load_3d(smem_u32(smem + C::OFF_K + c * 128 * 128), &tmK, bar, c * 64, t.hk,
                                     t.k_start + t.n0);
-                        tma_load_3d(smem_u32(smem + C::OFF_V + c * 128 * 128), &tmV, kv_full, c * 64, t.hk,
+                        tma_load_3d(smem_u32(smem + C::OFF_V + c * 128 * 128), &tmV, bar, c * 64, t.hk,
                                     t.k_start + t.n0);
                     }
+                }
+                if (k_past) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) { ok = false; break; }
+                    zero_rows<D / 64, 128, 32>(smem + C::OFF_K, t.Lk - t.n0, lane);
+                    zero_rows<D / 64, 128, 32>(smem + C::OFF_V, t.Lk - t.n0, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv_full);
                 }
                 ++unit_it;
                 for (int it = 0; it < t.n_it && ok; ++it) {
@@ -809,15 +839,24 @@ __global__ void __launch_bounds__(384, 1)
                             sLSE[st * 64 + qi] = in ? -__ldg(p.lse2 + idx) : -INFINITY;
                             sDel[st * 64 + qi] = in ? -__ldg(p.delta + idx) : 0.f;
                         }
+                        const bool past = MODE != kScorePlain && row0 + 64 > t.Lq;
+                        const uint32_t bar = past ? raw : q_full(st);
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(q_full(st), 2 * C::IT_BYTES);
+                            mbar_arrive_expect_tx(bar, 2 * C::IT_BYTES);
 #pragma unroll
                             for (int c = 0; c < D / 64; ++c) {
                                 tma_load_3d(smem_u32(smem + C::OFF_Q + st * C::IT_BYTES + c * 64 * 128), &tmQ,
-                                            q_full(st), c * 64, h, t.q_start + row0);
+                                            bar, c * 64, h, t.q_start + row0);
                                 tma_load_3d(smem_u32(smem + C::OFF_DO + st * C::IT_BYTES + c * 64 * 128), &tmDO,
-                                            q_full(st), c * 64, h, t.q_start + row0);
+                                            bar, c * 64, h, t.q_start + row0);
                             }
+                        }
+                        if (past) {
+                            if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) { ok = false; break; }
+                            zero_rows<D / 64, 64, 32>(smem + C::OFF_Q + st * C::IT_BYTES, t.Lq - row0, lane);
+                            zero_rows<D / 64, 64, 32>(smem + C::OFF_DO + st * C::IT_BYTES, t.Lq - row0, lane);
+                            fence_proxy_async_smem();
+                            if (lane == 0) mbar_arrive(q_full(st));   // in place of the loads' expect-tx
                         }
                         mbar_arrive(q_full(st));
                     }

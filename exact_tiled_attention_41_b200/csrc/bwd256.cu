@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(512, 1)
     auto stat_full = [&](uint32_t s) { return b0 + 8u * (C::BAR_STAT_FULL + s); };
     auto stat_empty = [&](uint32_t s) { return b0 + 8u * (C::BAR_STAT_EMPTY + s); };
     const uint32_t s_full = b0 + 8u * C::BAR_S_FULL, p_full = s_full + 8, dq_full = s_full + 16,
-                   dq_empty = s_full + 24, dkv_full = s_full + 32, dv_done = s_full + 40;
+                   dq_empty = s_full + 24, dkv_full = s_full + 32, dv_done = s_full + 40, raw = b0 + 8u * (C::NUM_BARS + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int PRODUCER = 12, MMA_A = 13, MMA_B = 14;
 
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(bars + C::BAR_FEED + s, 1);                              // unit published
             mbar_init(bars + C::BAR_FEED + kFeedSlots + s, DQ ? 14 : 10);      // read by the issuers, compute (, dQ) warps
         }
+        mbar_init(bars + C::NUM_BARS + 1, 1);   // raw: boxes that end past their sequence have arrived
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -214,17 +215,18 @@ __global__ void __launch_bounds__(512, 1)
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
         if (warp == PRODUCER) {
-            uint32_t unit_it = 0, q_it = 0;
+            uint32_t unit_it = 0, q_it = 0, raw_it = 0;
             bool ok = true;
             // head-dim chunks c0, c0 + 1 of a 64-row tile of Q or dO into the ring slot of pair number px
-            auto load_pair = [&](uint32_t px, const CUtensorMap* map, int c0, int h, int row) -> bool {
+            auto load_pair = [&](uint32_t px, const CUtensorMap* map, int c0, int h, int row, bool past) -> bool {
                 const uint32_t sl = px % C::NSLOT, n = px / C::NSLOT;
                 if (n > 0 && !mbar_wait(slot_empty(sl), (n - 1) & 1, w)) return false;
                 if (lane == 0) {
                     const uint32_t dst = smem_u32(smem + C::OFF_RING + sl * C::PAIR_BYTES);
-                    mbar_arrive_expect_tx(slot_full(sl), C::PAIR_BYTES);
-                    tma_load_3d(dst, map, slot_full(sl), c0 * 64, h, row);
-                    tma_load_3d(dst + C::BOX_BYTES, map, slot_full(sl), (c0 + 1) * 64, h, row);
+                    const uint32_t bar = past ? raw : slot_full(sl);
+                    if (!past) mbar_arrive_expect_tx(bar, C::PAIR_BYTES);
+                    tma_load_3d(dst, map, bar, c0 * 64, h, row);
+                    tma_load_3d(dst + C::BOX_BYTES, map, bar, (c0 + 1) * 64, h, row);
                 }
                 return true;
             };
@@ -254,8 +256,14 @@ __global__ void __launch_bounds__(512, 1)
                         nd[e] = in ? -__ldg(p.delta + idx) : 0.f;
                     }
                     const uint32_t px = 4u * q_it;
-                    if (!load_pair(px, &tmQ, 2 * oh, h, row) || !load_pair(px + 1, &tmDO, 2 * oh, h, row) ||
-                        !load_pair(px + 2, &tmQ, 2 * t.hh, h, row)) {
+                    // with score modifiers, rows past the sequences become zeros before the products read them: such
+                    // boxes arrive at `raw`, all of the tile's together
+                    const bool q_past = MODE != kScorePlain && m0 + 64 > t.Lq;
+                    const bool k_past = MODE != kScorePlain && it == 0 && t.n0 + 128 > t.Lk;
+                    if ((q_past || k_past) && lane == 0)
+                        mbar_arrive_expect_tx(raw, (q_past ? 4 * C::PAIR_BYTES : 0) + (k_past ? 2 * C::KV_BYTES : 0));
+                    if (!load_pair(px, &tmQ, 2 * oh, h, row, q_past) || !load_pair(px + 1, &tmDO, 2 * oh, h, row, q_past) ||
+                        !load_pair(px + 2, &tmQ, 2 * t.hh, h, row, q_past)) {
                         ok = false;
                         break;
                     }
@@ -263,18 +271,36 @@ __global__ void __launch_bounds__(512, 1)
                         // K and V of the unit, once the previous unit's last products have run
                         if (unit_it > 0 && !mbar_wait(kv_empty, (unit_it - 1) & 1, w)) { ok = false; break; }
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(kv_full, 2 * C::KV_BYTES);
+                            const uint32_t bar = k_past ? raw : kv_full;
+                            if (!k_past) mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                tma_load_3d(smem_u32(smem + C::OFF_K + c * 128 * 128), &tmK, kv_full, c * 64, t.hk,
+                                tma_load_3d(smem_u32(smem + C::OFF_K + c * 128 * 128), &tmK, bar, c * 64, t.hk,
                                             t.k_start + t.n0);
-                                tma_load_3d(smem_u32(smem + C::OFF_V + c * 128 * 128), &tmV, kv_full, c * 64, t.hk,
+                                tma_load_3d(smem_u32(smem + C::OFF_V + c * 128 * 128), &tmV, bar, c * 64, t.hk,
                                             t.k_start + t.n0);
                             }
                         }
                         ++unit_it;
                     }
-                    if (!load_pair(px + 3, &tmDO, 2 * t.hh, h, row)) { ok = false; break; }
+                    if (!load_pair(px + 3, &tmDO, 2 * t.hh, h, row, q_past)) { ok = false; break; }
+                    if (q_past || k_past) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) { ok = false; break; }
+                        if (q_past)
+                            for (uint32_t i = 0; i < 4; ++i)
+                                zero_rows<2, 64, 32>(smem + C::OFF_RING + (px + i) % C::NSLOT * C::PAIR_BYTES, t.Lq - m0, lane);
+                        if (k_past) {
+                            zero_rows<4, 128, 32>(smem + C::OFF_K, t.Lk - t.n0, lane);
+                            zero_rows<4, 128, 32>(smem + C::OFF_V, t.Lk - t.n0, lane);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (q_past)
+                                for (uint32_t i = 0; i < 4; ++i) mbar_arrive(slot_full((px + i) % C::NSLOT));
+                            if (k_past) mbar_arrive(kv_full);
+                        }
+                    }
                     const uint32_t sb = q_it & 1;
                     if (q_it >= 2 && !mbar_wait(stat_empty(sb), ((q_it >> 1) - 1) & 1, w)) { ok = false; break; }
 #pragma unroll

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(384, 1)
     auto s_full = [&](int s) { return b1 + 8u * s; };
     const uint32_t dp_full = b1 + 16, dp_free = b1 + 24;
     auto ds_full = [&](int s) { return b1 + 32 + 8u * s; };
-    const uint32_t dq_full = b1 + 48, dq_empty = b1 + 56;
+    const uint32_t dq_full = b1 + 48, dq_empty = b1 + 56, raw = b0 + 8u * (C::NUM_BARS + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(bars + C::B1 + 5, 256);   // ds_full[1]
         mbar_init(bars + C::B1 + 6, 1);     // dq_full
         mbar_init(bars + C::B1 + 7, 256);   // dq_empty
+        mbar_init(bars + C::NUM_BARS + 1, 1);   // raw: a K or V tile that ends past its sequence has arrived
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -187,36 +188,58 @@ __global__ void __launch_bounds__(384, 1)
     const Watch w{abort_flag, p.status, p.timeout_ns};
 
     if (warp == PRODUCER) {
-        if (lane == 0) {
-            uint32_t kv_it = 0, q_it = 0;
+        // with score modifiers the whole warp goes through the loop: it clears the rows of K and V past a sequence
+        constexpr bool WARP = MODE != kScorePlain;
+        if (WARP || lane == 0) {
+            uint32_t kv_it = 0, q_it = 0, raw_it = 0;
+            auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+                const bool got = mbar_wait(bar, parity, w);
+                if constexpr (WARP) return __all_sync(0xffffffffu, got);
+                return got;
+            };
             bool ok = true;
             for (int k = 0, u = snake_unit(0, p.num_units); u >= 0 && ok; u = snake_unit(++k, p.num_units)) {
                 if (u >= p.num_units) continue;
                 const DqUnit t = decode_dq_unit<BK>(p, u);
                 if (t.skip || t.n_kv == 0) continue;
                 const int hk = t.h / p.group;
-                if (q_it > 0 && !mbar_wait(q_empty, (q_it - 1) & 1, w)) break;
-                mbar_arrive_expect_tx(q_full, 2 * C::T_BYTES);
+                if (q_it > 0 && !wait(q_empty, (q_it - 1) & 1)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, 2 * C::T_BYTES);
 #pragma unroll
-                for (int c = 0; c < C::NCHUNK; ++c) {
-                    tma_load_3d(smem_u32(sQ + c * BM * 128), &tmQ, q_full, c * 64, t.h, t.q_start + t.q0);
-                    tma_load_3d(smem_u32(sDO + c * BM * 128), &tmDO, q_full, c * 64, t.h, t.q_start + t.q0);
+                    for (int c = 0; c < C::NCHUNK; ++c) {
+                        tma_load_3d(smem_u32(sQ + c * BM * 128), &tmQ, q_full, c * 64, t.h, t.q_start + t.q0);
+                        tma_load_3d(smem_u32(sDO + c * BM * 128), &tmDO, q_full, c * 64, t.h, t.q_start + t.q0);
+                    }
                 }
                 ++q_it;
                 for (int j = 0; j < t.n_kv; ++j, ++kv_it) {
                     const int st = kv_it % KST, sv = kv_it % VST;
                     const uint32_t n = kv_it / KST, nv = kv_it / VST;
                     const int krow = t.k_start + (t.kv0 + j) * BK;
-                    if (n > 0 && !mbar_wait(k_empty(st), (n - 1) & 1, w)) { ok = false; break; }
-                    mbar_arrive_expect_tx(k_full(st), C::KV_BYTES);
+                    const int inside = t.Lk - (t.kv0 + j) * BK;   // rows of the tile in the sequence
+                    auto load = [&](uint8_t* tile, const CUtensorMap* map, uint32_t full) -> bool {
+                        const bool past = WARP && inside < BK;
+                        if (lane == 0) {
+                            const uint32_t bar = past ? raw : full;
+                            mbar_arrive_expect_tx(bar, C::KV_BYTES);
 #pragma unroll
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_3d(smem_u32(sK + st * C::KV_BYTES + c * BK * 128), &tmK, k_full(st), c * 64, hk, krow);
-                    if (nv > 0 && !mbar_wait(v_empty(sv), (nv - 1) & 1, w)) { ok = false; break; }
-                    mbar_arrive_expect_tx(v_full(sv), C::KV_BYTES);
-#pragma unroll
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_3d(smem_u32(sV + sv * C::KV_BYTES + c * BK * 128), &tmV, v_full(sv), c * 64, hk, krow);
+                            for (int c = 0; c < C::NCHUNK; ++c)
+                                tma_load_3d(smem_u32(tile + c * BK * 128), map, bar, c * 64, hk, krow);
+                        }
+                        if (past) {
+                            if (!wait(raw, raw_it++ & 1)) return false;
+                            zero_rows<C::NCHUNK, BK, 32>(tile, inside, lane);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(full);
+                        }
+                        return true;
+                    };
+                    if (n > 0 && !wait(k_empty(st), (n - 1) & 1)) { ok = false; break; }
+                    if (!load(sK + st * C::KV_BYTES, &tmK, k_full(st))) { ok = false; break; }
+                    if (nv > 0 && !wait(v_empty(sv), (nv - 1) & 1)) { ok = false; break; }
+                    if (!load(sV + sv * C::KV_BYTES, &tmV, v_full(sv))) { ok = false; break; }
                 }
             }
         }
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(384, 1)
                     uint32_t sv[32];
                     tmem_ld32(tS + cc * 32, sv);
                     tmem_ld_wait_tie(sv);
-                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sv, p.sc);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sv, p.sc, valid);
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {

@@ -225,9 +225,10 @@ __host__ __device__ constexpr bool fixed_reference(int mode) { return (mode & kS
 // One tile of a row against its fixed reference: P = exp2(c2 tanh(in s) + bias - reference) for the BK scores at
 // tS, written over them as packed bf16; returns the row's sum.  Columns lo .. hi are allowed (masked: some are
 // not); column c lies at distance d0 - c from the row; the reference is the bias at distance d_ref and sc.ref_log2.
+// A row past its sequence is not valid: it has no part in the warp's choice of tanh polynomial.
 template <int BK, int MODE>
 __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& sc, float slope, int d0, int d_ref,
-                                               bool past, bool masked, int lo, int hi) {
+                                               bool past, bool masked, int lo, int hi, bool valid) {
     float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
     uint32_t s[2][32];
     float (&x)[64] = reinterpret_cast<float (&)[64]>(s);
@@ -240,7 +241,7 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
         tmem_ld32(tS + c0 + 32, s[1]);
         tmem_ld_wait_tie(s[0]);
         reg_tie(s[1]);
-        const float most = max_abs(x);
+        const float most = valid ? max_abs(x) : 0.f;
         if (masked) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) x[c] = (c0 + c >= lo && c0 + c <= hi) ? x[c] : -INFINITY;
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
     auto k_empty = [&](int s) { return bar0 + 8u * (5 * NQ + KST + s); };
     auto v_full = [&](int s) { return bar0 + 8u * (5 * NQ + 2 * KST + s); };
     auto v_empty = [&](int s) { return bar0 + 8u * (5 * NQ + 3 * KST + s); };
+    const uint32_t raw = bar0 + 8u * (C::NUM_BARS + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             mbar_init(bars + 5 * NQ + 4 * KST + s, 1);                       // unit published
             mbar_init(bars + 5 * NQ + 4 * KST + kFeedSlots + s, 1 + 4 * NQ); // read by the MMA and softmax warps
         }
+        mbar_init(bars + C::NUM_BARS + 1, 1);   // raw: K and V tiles that end past their sequence have arrived
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -368,14 +371,33 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
     if (warp >= 4 * NQ) {
     if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == PRODUCER) {
-        if (lane == 0) {
-            uint32_t kv_it = 0, q_it = 0;
+        // with score modifiers the whole warp goes through the loop: it clears the rows of K and V past
+        // a sequence, which may hold NaN (P = 0 there, but 0 x NaN is NaN) and would take part in the warps' votes
+        constexpr bool WARP = MODE != kScorePlain;
+        if (WARP || lane == 0) {
+            uint32_t kv_it = 0, q_it = 0, raw_it = 0;
+            auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+                const bool got = mbar_wait(bar, parity, w);
+                if constexpr (WARP) return __all_sync(0xffffffffu, got);
+                return got;
+            };
+            // K and V of such a tile arrive together, in one phase of `raw`, except with a single stage: there V's slot is
+            // released after the product that waits for K
+            constexpr bool TOGETHER = KST > 1;
+            auto clean = [&](uint8_t* stages, uint32_t full, int st, int inside) {
+                zero_rows<C::NCHUNK, BK, 32>(stages + st * C::KV_BYTES, inside, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            };
             // DYN: units come from the counter; the next one is taken and published one ahead of the one
             // being loaded, so the counter's latency is hidden.  Static: the boustrophedon deal.
             int k_static = 0;
             auto take = [&]() -> int {
                 if constexpr (DYN) {
-                    const int v = atomicAdd(p.counter, 1);
+                    int v = 0;
+                    if (lane == 0) v = atomicAdd(p.counter, 1);
+                    if constexpr (WARP) v = __shfl_sync(0xffffffffu, v, 0);
                     return v < p.num_units ? v : -1;
                 } else {
                     return snake_unit(k_static++, p.num_units);   // -1 at the end, num_units = an empty slot
@@ -384,9 +406,11 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             auto publish = [&](uint32_t it, int v) -> bool {
                 if constexpr (!DYN) return true;
                 const uint32_t s = it % kFeedSlots;
-                if (it >= kFeedSlots && !mbar_wait(feed.empty0 + 8 * s, ((it / kFeedSlots) - 1) & 1, w)) return false;
-                feed.slot[s] = v;
-                mbar_arrive(feed.full0 + 8 * s);
+                if (it >= kFeedSlots && !wait(feed.empty0 + 8 * s, ((it / kFeedSlots) - 1) & 1)) return false;
+                if (lane == 0) {
+                    feed.slot[s] = v;
+                    mbar_arrive(feed.full0 + 8 * s);
+                }
                 return true;
             };
             int u_next = take();
@@ -400,8 +424,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 if (t.skip || t.n_kv == 0) continue;
                 const int hk = t.h / p.group;
                 for (int i = 0; i < NQ && ok; ++i) {
-                    if (q_it > 0 && !mbar_wait(q_empty(i), (q_it - 1) & 1, w)) ok = false;
+                    if (q_it > 0 && !wait(q_empty(i), (q_it - 1) & 1)) ok = false;
                     if (!ok) break;
+                    if (lane != 0) continue;
                     mbar_arrive_expect_tx(q_full(i), C::Q_BYTES);
 #pragma unroll
                     for (int c = 0; c < C::NCHUNK; ++c)
@@ -413,18 +438,35 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 for (int j = 0; j < t.n_kv && ok; ++j, ++kv_it) {
                     const int st = kv_it % KST;
                     const uint32_t n = kv_it / KST;
-                    if (n > 0 && !mbar_wait(k_empty(st), (n - 1) & 1, w)) { ok = false; break; }
-                    mbar_arrive_expect_tx(k_full(st), C::KV_BYTES);
+                    if (n > 0 && !wait(k_empty(st), (n - 1) & 1)) { ok = false; break; }
+                    const int inside = t.Lk - unit_tile<LOCAL, REV>(t, j) * BK;   // rows of the tile in the sequence
+                    const bool past = WARP && inside < BK;
+                    if (lane == 0) {
+                        const uint32_t bar = past ? raw : k_full(st);
+                        mbar_arrive_expect_tx(bar, past && TOGETHER ? 2 * C::KV_BYTES : C::KV_BYTES);
 #pragma unroll
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_3d(smem_u32(sK + st * C::KV_BYTES + c * BK * 128), &tmK, k_full(st), c * 64, hk,
-                                    t.k_start + unit_tile<LOCAL, REV>(t, j) * BK);
-                    if (n > 0 && !mbar_wait(v_empty(st), (n - 1) & 1, w)) { ok = false; break; }
-                    mbar_arrive_expect_tx(v_full(st), C::KV_BYTES);
+                        for (int c = 0; c < C::NCHUNK; ++c)
+                            tma_load_3d(smem_u32(sK + st * C::KV_BYTES + c * BK * 128), &tmK, bar, c * 64, hk,
+                                        t.k_start + unit_tile<LOCAL, REV>(t, j) * BK);
+                    }
+                    if (past && !TOGETHER) {
+                        if (!wait(raw, raw_it++ & 1)) { ok = false; break; }
+                        clean(sK, k_full(st), st, inside);
+                    }
+                    if (n > 0 && !wait(v_empty(st), (n - 1) & 1)) { ok = false; break; }
+                    if (lane == 0) {
+                        const uint32_t bar = past ? raw : v_full(st);
+                        if (!past || !TOGETHER) mbar_arrive_expect_tx(bar, C::KV_BYTES);
 #pragma unroll
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_3d(smem_u32(sV + st * C::KV_BYTES + c * BK * 128), &tmV, v_full(st), c * 64, hk,
-                                    t.k_start + unit_tile<LOCAL, REV>(t, j) * BK);
+                        for (int c = 0; c < C::NCHUNK; ++c)
+                            tma_load_3d(smem_u32(sV + st * C::KV_BYTES + c * BK * 128), &tmV, bar, c * 64, hk,
+                                        t.k_start + unit_tile<LOCAL, REV>(t, j) * BK);
+                    }
+                    if (past) {
+                        if (!wait(raw, raw_it++ & 1)) { ok = false; break; }
+                        if (TOGETHER) clean(sK, k_full(st), st, inside);
+                        clean(sV, v_full(st), st, inside);
+                    }
                 }
                 if (!ok) break;
             }
@@ -586,7 +628,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
                 if constexpr (FIXED) {
                     l += softmax_fixed<BK, MODE>(tS, p.sc, slope, at - kbase, d_ref, p.wr == 0, masked, key_lo - kbase,
-                                                 key_hi - kbase);
+                                                 key_hi - kbase, valid);
                 } else {
                 float s[BK];
                 {
@@ -600,7 +642,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                     for (int cc = 1; cc < BK / 32; ++cc) reg_tie(*reinterpret_cast<uint32_t(*)[32]>(sr + cc * 32));
                 }
                 float shift = 0.f;   // the row's part of the bias
-                if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc);
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc, valid);
                 if constexpr ((MODE & kScoreBias) != 0)
                     shift = bias_scores(s, slope, static_cast<float>(at - kbase), p.wr == 0);
                 if (masked) {
@@ -613,6 +655,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                 for (int c = 4; c < BK; c += 2) mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], s[c], s[c + 1]);
                 float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                 if constexpr ((MODE & kScoreBias) != 0) mt += shift;
+                if (MODE != kScorePlain && !valid) mt = -INFINITY;   // rows past the sequence have no say
                 const bool need = (mt - m_ref) * c2 > kDeferLog2;   // NaN (both -inf) -> false
                 if (__any_sync(0xffffffffu, need)) {
                     const float m_new = fmaxf(m_ref, mt);

@@ -153,10 +153,11 @@ __device__ __forceinline__ float max_abs(const float (&s)[N]) {
     return fmaxf(m[0], m[1]);
 }
 
-// s <- tanh(in * s) for a thread's block of raw scores
+// s <- tanh(in * s) for a thread's block of raw scores; a thread that is not valid (a row past its sequence) has no
+// part in the warp's choice of polynomial
 template <int N>
-__device__ __forceinline__ void cap_scores(float (&s)[N], const ScoreParams& sc) {
-    with_tanh_range(max_abs(s), sc, [&](auto range) {
+__device__ __forceinline__ void cap_scores(float (&s)[N], const ScoreParams& sc, bool valid = true) {
+    with_tanh_range(valid ? max_abs(s) : 0.f, sc, [&](auto range) {
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             const float2 t = cap_pair<decltype(range)::value>(make_float2(s[e], s[e + 1]), splat2(sc.in));
@@ -166,8 +167,8 @@ __device__ __forceinline__ void cap_scores(float (&s)[N], const ScoreParams& sc)
     });
 }
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreParams& sc) {
-    cap_scores(reinterpret_cast<float (&)[N]>(s), sc);
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreParams& sc, bool valid = true) {
+    cap_scores(reinterpret_cast<float (&)[N]>(s), sc, valid);
 }
 
 // slope * log2(e) of query head h of sequence b

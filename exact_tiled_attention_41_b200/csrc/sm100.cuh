@@ -132,6 +132,17 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Zeros in rows first .. ROWS - 1 of BOXES boxes of ROWS x 128 bytes, by the threads tid = 0 .. THREADS - 1.  A tile
+// that ends past its sequence holds rows of the next one, or of none, and 0 x NaN would reach the result.
+template <int BOXES, int ROWS, int THREADS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int first, int tid) {
+    first = max(first, 0);
+#pragma unroll 1
+    for (int e = first * 8 + tid; e < ROWS * 8; e += THREADS)
+#pragma unroll
+        for (int c = 0; c < BOXES; ++c) *reinterpret_cast<uint4*>(tile + c * ROWS * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+}
+
 // ------------------------------------------------------------------ tensor memory
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)

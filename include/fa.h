@@ -270,6 +270,9 @@ FA_API int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const 
  * Sk and Sq are the lengths of the sequence (varlen: of each; cache: keys attended to,
  * and Sq).  Distances are formed in float32, exact up to 2^24 tokens.
  * The backward needs the out and lse of the forward with the same modifiers.
+ * Rows outside a sequence (its neighbours, padding behind the last) may hold anything,
+ * NaN included: they change no bit of it.  (The plain calls need them finite where a
+ * 128-row tile reaches past a sequence.)
  * Workspaces and their sizes are those of the plain calls.
  */
 FA_API int fa_fwd_mod(const void* q, const void* k, const void* v, void* out, float* lse,

@@ -278,3 +278,59 @@ def test_cache(D, softcap, kind, Sq, new, page, causal, window):
 def test_cache_does_not_depend_on_the_split(num_splits):
     w = W.kvcache_update(2, 4, 7, 7, 128, 2048, [2044, 513], seqlen_new=4, seed=8)
     check_cache(w, True, NONE, 8.0, slopes_of(7), num_splits)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap,kind", MODS + [(80.0, "falling")])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_rows_outside_a_sequence_do_not_reach_it(D, softcap, kind, bad):
+    """A neighbouring sequence full of NaN or infinities, and such padding behind the last one, change no bit of the
+    others (dq of the backward that adds in any order: within two roundings)."""
+    lq, lk = [130, 57, 70], [140, 57, 33]
+    w = W.varlen(lq + [20], lk + [20], 4, 2, D, True, seed=D)
+    good = {n: x.cuda() for n, x in w.tensors.items()}
+    cq, ck = (torch.tensor(np.cumsum([0] + n), dtype=torch.int32) for n in (lq, lk))
+    filled = {n: x.clone() for n, x in good.items()}
+    for n, cu in (("q", cq), ("k", ck), ("v", ck), ("do", cq)):
+        filled[n][cu[1]:cu[2]] = bad
+        filled[n][cu[3]:] = bad
+    sl = None if kind is None else slopes_of(4, kind=kind).cuda()
+    where = (cq.cuda(), ck.cuda(), max(lq), max(lk))
+    for causal, window, det in ((True, NONE, True), (False, (20, 10), False), (False, (3, 2), True)):
+        res = []
+        for t in (good, filled):
+            out, lse = A.flash_attn_varlen_func(t["q"], t["k"], t["v"], *where, w.scale, causal, window, softcap, sl)
+            res.append((out, lse.t()) + A.flash_attn_varlen_backward(t["do"], t["q"], t["k"], t["v"], out, lse, *where,
+                                                                     w.scale, causal, window, det, softcap, sl))
+        assert abi.fa_get_device_status() == 0
+        for name, a, b, cu in zip(("o", "lse", "dq", "dk", "dv"), *res, (cq, cq, cq, ck, ck)):
+            for s in (0, 2):
+                x, y = a[cu[s]:cu[s + 1]], b[cu[s]:cu[s + 1]]
+                if name == "dq" and not det:
+                    assert ((x.float() - y.float()).abs() <= 2.0 ** -7 * x.float().abs() + 1e-5).all()
+                else:
+                    assert torch.equal(x, y), name
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_padding_behind_the_last_sequence_is_left_as_it_was(D):
+    lq, lk = [3, 130], [130, 65]
+    w = W.varlen(lq + [9], lk + [9], 4, 2, D, True, seed=D + 1)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    cq, ck = (torch.tensor(np.cumsum([0] + n), dtype=torch.int32).cuda() for n in (lq, lk))
+    out, lse = torch.full_like(t["q"], 7.0), torch.full((4, t["q"].shape[0]), 7.0, device="cuda")
+    grads = [torch.full_like(t[n], 7.0) for n in ("q", "k", "v")]
+    sl = slopes_of(4).cuda()
+    nb = abi.fa_varlen_bwd_workspace_size(2, t["q"].shape[0], t["k"].shape[0], 4, 2, D)
+    ws = torch.empty(max(nb, 256), dtype=torch.uint8, device="cuda")
+    sizes = (2, max(lq), max(lk), t["q"].shape[0], t["k"].shape[0], 4, 2, D, w.scale, True, -1, -1)
+    assert abi.fa_varlen_fwd_mod(t["q"], t["k"], t["v"], out, lse, cq, ck, *sizes, 5.0, sl, 0, ws, nb) == 0
+    for det in (False, True):
+        assert abi.fa_varlen_bwd_mod(t["q"], t["k"], t["v"], out, t["do"], lse, *grads, cq, ck, *sizes, det, 5.0, sl, 0, ws, nb) == 0
+        for x, n in ((out, 133), (lse.t(), 133), (grads[0], 133), (grads[1], 195), (grads[2], 195)):
+            # the backward that adds into an fp32 dq converts all of its rows: zeros there, with and without modifiers
+            zeros = x is grads[0] and not det
+            assert (x[n:] == (0.0 if zeros else 7.0)).all() and (x[:n] != 7.0).any()
+            if zeros:
+                x.fill_(7.0)
+    assert abi.fa_get_device_status() == 0
