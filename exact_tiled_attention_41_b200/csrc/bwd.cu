@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(512, 1)
                     const int m0 = (t.m_start + it % t.n_m) * 128;
                     const int h = t.hk * G + g;
                     const int st = q_it % ST;
-                    if (q_it >= ST && !mbar_wait(q_empty(st), ((q_it / ST) - 1) & 1, w)) return false;
+                    if (q_it >= ST && !mbar_wait_warp(q_empty(st), ((q_it / ST) - 1) & 1, w)) return false;
                     // tile statistics; rows past the sequence get LSE2 = +inf (P = 0) and Delta = 0
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     if (past) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) return false;
+                        if (!mbar_wait_warp(raw, raw_it++ & 1, w)) return false;
                         zero_rows<C::NCHUNK, 128, 32>(smem + C::OFF_Q + st * C::T_BYTES, t.Lq - m0, lane);
                         zero_rows<C::NCHUNK, 128, 32>(smem + C::OFF_DO + st * C::T_BYTES, t.Lq - m0, lane);
                         fence_proxy_async_smem();
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(512, 1)
                             tma_load_3d(smem_u32(smem + off + c * 128 * 128), map, bar, c * 64, t.hk, t.k_start + t.n0);
                     }
                     if (past) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) return false;
+                        if (!mbar_wait_warp(raw, raw_it++ & 1, w)) return false;
                         zero_rows<C::NCHUNK, 128, 32>(smem + off, t.Lk - t.n0, lane);
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -332,10 +332,10 @@ __global__ void __launch_bounds__(512, 1)
                     return true;
                 };
                 // V (free once the previous unit's last dP^T has run), the first Q / dO tile, then K
-                if (unit_it > 0 && !mbar_wait(v_free, (unit_it - 1) & 1, w)) { ok = false; break; }
+                if (unit_it > 0 && !mbar_wait_warp(v_free, (unit_it - 1) & 1, w)) { ok = false; break; }
                 if (!load_kv(C::OFF_V, &tmV, v_full)) { ok = false; break; }
                 if (!load_tile(0)) { ok = false; break; }
-                if (unit_it > 0 && !mbar_wait(k_free, (unit_it - 1) & 1, w)) { ok = false; break; }
+                if (unit_it > 0 && !mbar_wait_warp(k_free, (unit_it - 1) & 1, w)) { ok = false; break; }
                 if (!load_kv(C::OFF_K, &tmK, k_full)) { ok = false; break; }
                 ++unit_it;
                 for (int it = 1; it < t.n_it && ok; ++it)
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(512, 1)
                 const int h = t.hk * G + g;
                 const bool valid = m0 + r < t.Lq;
                 const size_t tok = static_cast<size_t>(t.q_start) + m0 + r;
-                if (!mbar_wait(dq_full, g_it & 1, w)) { ok = false; break; }
+                if (!mbar_wait_warp(dq_full, g_it & 1, w)) { ok = false; break; }
                 tc_fence_after();
                 float4* acc = reinterpret_cast<float4*>(p.dq_acc) + static_cast<size_t>(h) * (D / 4) * p.Tq + tok;
                 // the whole dQ row in registers at once, so its columns are released before the reduce-adds
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(512, 1)
             }
             if (!ok) break;
             // -------------------------------------------------- epilogue: warpgroup 0 writes dV, 1 writes dK
-            if (!mbar_wait(dkv_full, unit_it & 1, w)) { ok = false; break; }
+            if (!mbar_wait_warp(dkv_full, unit_it & 1, w)) { ok = false; break; }
             ++unit_it;
             tc_fence_after();
             const uint32_t col = gq == 0 ? C::COL_DV : C::COL_DK;
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (u >= p.num_units) continue;
                 const BUnit t = decode_bunit(p, u);
                 if (t.skip || t.n_it == 0) continue;
-                if (unit_it > 0 && !mbar_wait(kv_empty, (unit_it - 1) & 1, w)) { ok = false; break; }
+                if (unit_it > 0 && !mbar_wait_warp(kv_empty, (unit_it - 1) & 1, w)) { ok = false; break; }
                 // tiles that end past their sequence are cleaned as in bwd_kernel
                 const bool k_past = MODE != kScorePlain && t.n0 + 128 > t.Lk;
                 if (lane == 0) {
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 if (k_past) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) { ok = false; break; }
+                    if (!mbar_wait_warp(raw, raw_it++ & 1, w)) { ok = false; break; }
                     zero_rows<D / 64, 128, 32>(smem + C::OFF_K, t.Lk - t.n0, lane);
                     zero_rows<D / 64, 128, 32>(smem + C::OFF_V, t.Lk - t.n0, lane);
                     fence_proxy_async_smem();
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int qh = 0; qh < 2; ++qh, ++q_it) {
                         const int row0 = (t.m_start + it % t.n_m) * 128 + 64 * qh;
                         const int st = q_it % ST;
-                        if (q_it >= ST && !mbar_wait(q_empty(st), ((q_it / ST) - 1) & 1, w)) { ok = false; break; }
+                        if (q_it >= ST && !mbar_wait_warp(q_empty(st), ((q_it / ST) - 1) & 1, w)) { ok = false; break; }
                         // item statistics; rows past the sequence get LSE2 = +inf (P = 0) and Delta = 0
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(384, 1)
                             }
                         }
                         if (past) {
-                            if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) { ok = false; break; }
+                            if (!mbar_wait_warp(raw, raw_it++ & 1, w)) { ok = false; break; }
                             zero_rows<D / 64, 64, 32>(smem + C::OFF_Q + st * C::IT_BYTES, t.Lq - row0, lane);
                             zero_rows<D / 64, 64, 32>(smem + C::OFF_DO + st * C::IT_BYTES, t.Lq - row0, lane);
                             fence_proxy_async_smem();
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!ok) break;
             // -------------------------------------------------- epilogue: warpgroup 0 writes dV, 1 writes dK
-            if (!mbar_wait(dkv_full, unit_it & 1, w)) { ok = false; break; }
+            if (!mbar_wait_warp(dkv_full, unit_it & 1, w)) { ok = false; break; }
             ++unit_it;
             tc_fence_after();
             const uint32_t col = gb == 0 ? C::COL_DV : C::COL_DK;

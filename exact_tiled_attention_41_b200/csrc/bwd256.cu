@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(512, 1)
             // head-dim chunks c0, c0 + 1 of a 64-row tile of Q or dO into the ring slot of pair number px
             auto load_pair = [&](uint32_t px, const CUtensorMap* map, int c0, int h, int row, bool past) -> bool {
                 const uint32_t sl = px % C::NSLOT, n = px / C::NSLOT;
-                if (n > 0 && !mbar_wait(slot_empty(sl), (n - 1) & 1, w)) return false;
+                if (n > 0 && !mbar_wait_warp(slot_empty(sl), (n - 1) & 1, w)) return false;
                 if (lane == 0) {
                     const uint32_t dst = smem_u32(smem + C::OFF_RING + sl * C::PAIR_BYTES);
                     const uint32_t bar = past ? raw : slot_full(sl);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     if (it == 0) {
                         // K and V of the unit, once the previous unit's last products have run
-                        if (unit_it > 0 && !mbar_wait(kv_empty, (unit_it - 1) & 1, w)) { ok = false; break; }
+                        if (unit_it > 0 && !mbar_wait_warp(kv_empty, (unit_it - 1) & 1, w)) { ok = false; break; }
                         if (lane == 0) {
                             const uint32_t bar = k_past ? raw : kv_full;
                             if (!k_past) mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     if (!load_pair(px + 3, &tmDO, 2 * t.hh, h, row, q_past)) { ok = false; break; }
                     if (q_past || k_past) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(raw, raw_it++ & 1, w))) { ok = false; break; }
+                        if (!mbar_wait_warp(raw, raw_it++ & 1, w)) { ok = false; break; }
                         if (q_past)
                             for (uint32_t i = 0; i < 4; ++i)
                                 zero_rows<2, 64, 32>(smem + C::OFF_RING + (px + i) % C::NSLOT * C::PAIR_BYTES, t.Lq - m0, lane);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     const uint32_t sb = q_it & 1;
-                    if (q_it >= 2 && !mbar_wait(stat_empty(sb), ((q_it >> 1) - 1) & 1, w)) { ok = false; break; }
+                    if (q_it >= 2 && !mbar_wait_warp(stat_empty(sb), ((q_it >> 1) - 1) & 1, w)) { ok = false; break; }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         sStat[sb * 128 + lane * 2 + e] = nl[e];
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(512, 1)
                     const int g = it / t.n_m;
                     const int m0 = (t.m_start + it % t.n_m) * 64;
                     const int h = t.hk * G + g;
-                    if (!mbar_wait(dq_full, q_it & 1, w)) { ok = false; break; }
+                    if (!mbar_wait_warp(dq_full, q_it & 1, w)) { ok = false; break; }
                     tc_fence_after();
 #if FA_B256_VEC_DQ
                     // lanes 4g .. 4g+3 hold head-dim rows 4g .. 4g+3; a 4 x 4 transpose across them (two
@@ -506,9 +506,10 @@ __global__ void __launch_bounds__(512, 1)
             if (p.wl >= 0) q_hi = kj - (t.Lk - t.Lq) + p.wl;
             for (int it = 0; it < t.n_it; ++it, ++q_it) {
                 const int m0 = (t.m_start + it % t.n_m) * 64;
-                if (!mbar_wait(s_full, q_it & 1, w)) { ok = false; break; }
                 const uint32_t sb = q_it & 1;
-                if (!mbar_wait(stat_full(sb), (q_it >> 1) & 1, w)) { ok = false; break; }
+                bool got = mbar_wait(s_full, q_it & 1, w);
+                got = got && mbar_wait(stat_full(sb), (q_it >> 1) & 1, w);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 const float* nL = sStat + sb * 128 + 32 * gq;      // -LSE2 of this warpgroup's 32 rows
                 const float* nD = nL + 64;                         // -Delta
                 tc_fence_after();
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(512, 1)
                 mbar_arrive(p_full);
             }
             if (!ok) break;
-            if (!mbar_wait(dkv_full, unit_it & 1, w)) { ok = false; break; }
+            if (!mbar_wait_warp(dkv_full, unit_it & 1, w)) { ok = false; break; }
             ++unit_it;
             tc_fence_after();
             const uint32_t col = gq == 0 ? C::COL_DV : C::COL_DK;

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             gt += t.n_kv;
             // ------------------------------------------------ epilogue: dq = bf16(scale * dQ), this warpgroup's half
-            if (!mbar_wait(dq_full, unit_it & 1, w)) { ok = false; break; }
+            if (!mbar_wait_warp(dq_full, unit_it & 1, w)) { ok = false; break; }
             ++unit_it;
             tc_fence_after();
             const float2 sc = make_float2(p.scale, p.scale);

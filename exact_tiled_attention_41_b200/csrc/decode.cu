@@ -247,7 +247,7 @@ __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
 
     for (int s = 0; s < ns; ++s) {
         const int slot = s % kDecStages;
-        if (!mbar_wait(full0 + 8 * slot, (s / kDecStages) & 1, w)) { ok = false; break; }
+        if (!mbar_wait_warp(full0 + 8 * slot, (s / kDecStages) & 1, w)) { ok = false; break; }
         const uint32_t sk = smem_u32(smem + slot * STAGE_BYTES);
         const uint32_t sv = sk + TILE_BYTES;
         const int kt = kstart + s * kDecTile + kw;    // logical index of this warp's first key

@@ -621,11 +621,13 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             float m_ref = -INFINITY;
             float l = 0.f;
             for (int j = 0; j < n_mine; ++j) {
-                if (!mbar_wait(s_full(i), s_it & 1, w)) { ok = false; break; }
+                // one vote for the mask and for the wait; a second one, on masked tiles, tells them apart
+                const bool got = mbar_wait(s_full(i), s_it & 1, w);
+                const int kbase = unit_tile<LOCAL, REV>(t, lo_i + j) * BK;
+                const bool masked = __any_sync(0xffffffffu, !got | (kbase + BK - 1 > key_hi) | (LOCAL && kbase < key_lo));
+                if (masked && !__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++s_it;
                 tc_fence_after();
-                const int kbase = unit_tile<LOCAL, REV>(t, lo_i + j) * BK;
-                const bool masked = __any_sync(0xffffffffu, kbase + BK - 1 > key_hi || (LOCAL && kbase < key_lo));
                 if constexpr (FIXED) {
                     l += softmax_fixed<BK, MODE>(tS, p.sc, slope, at - kbase, d_ref, p.wr == 0, masked, key_lo - kbase,
                                                  key_hi - kbase, valid);
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
             if (!ok) break;
             pv_total += n_mine;
             // ------------------------------------------------ epilogue: O / l, LSE
-            if (!mbar_wait(o_full(i), (pv_total - 1) & 1, w)) { ok = false; break; }
+            if (!mbar_wait_warp(o_full(i), (pv_total - 1) & 1, w)) { ok = false; break; }
             tc_fence_after();
             const float inv_l = l > 0.f ? 1.f / l : 0.f;
             uint32_t ro[32];

@@ -78,6 +78,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
     }
 }
 
+// The same for a whole warp whose lanes stay together.  A limit that expires, or an abort seen, while the barrier
+// flips would let some lanes go on and others leave, and the next warp-wide instruction would then name lanes that are
+// not there; the vote makes one answer of it.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Watch& w) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -505,7 +512,8 @@ __device__ __forceinline__ bool feed_put(const UnitFeed& f, uint32_t it, int* co
 // whole warp must call it together, or only lane 0 when the warp's other lanes never consume).
 __device__ __forceinline__ bool feed_get(const UnitFeed& f, uint32_t it, int& u, const Watch& w, bool whole_warp) {
     const uint32_t s = it % kFeedSlots;
-    if (!mbar_wait(f.full0 + 8 * s, (it / kFeedSlots) & 1, w)) return false;
+    const uint32_t full = f.full0 + 8 * s, parity = (it / kFeedSlots) & 1;
+    if (!(whole_warp ? mbar_wait_warp(full, parity, w) : mbar_wait(full, parity, w))) return false;
     u = f.slot[s];
     if (whole_warp) __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(f.empty0 + 8 * s);
