@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(512, 1)
                     tmem_ld32(tmem + lb + C::COL_DP + 64 * gq + 32 * half, dh);
                     tmem_ld_wait_tie(sh);
                     reg_tie(dh);
-                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores<(MODE & kScoreWide) != 0>(sh, p.sc);
                     uint32_t pp[16], dd[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_ld32(tmem + lb + C::COL_DP(gb) + 32 * half, dh);
                         tmem_ld_wait_tie(sh);
                         reg_tie(dh);
-                        if constexpr ((MODE & kScoreCap) != 0) cap_scores(sh, p.sc);
+                        if constexpr ((MODE & kScoreCap) != 0) cap_scores<(MODE & kScoreWide) != 0>(sh, p.sc);
                         uint32_t pp[16], dd[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -1444,7 +1444,7 @@ int launch_bwd(const Problem& pr, const void* out, const void* dout, const float
             default: return 2;
         }
     };
-    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
+    return with_score_mode(pr.softcap, pr.slopes, run);
 }
 
 }  // namespace fa

@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(512, 1)
                 tmem_ld32(tmem + lb + C::COL_DP + 32 * gq, da);
                 tmem_ld_wait_tie(sa);
                 reg_tie(da);
-                if constexpr ((MODE & kScoreCap) != 0) cap_scores(sa, p.sc);
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores<(MODE & kScoreWide) != 0>(sa, p.sc);
                 float slope = 0.f, d0 = 0.f;   // distance of the warpgroup's first query column from the key
                 if constexpr ((MODE & kScoreBias) != 0) {
                     slope = slope_log2(p.sc, t.b, t.hk * G + it / t.n_m);
@@ -694,7 +694,7 @@ int launch_bwd256_main(const Problem& pr, const void* dout, const float* lse2, c
         return with_dq ? run_bwd256<true, MODE>(pr, dout, lse2, delta, dq_acc, dq, dk, dv, dev, stream)
                        : run_bwd256<false, MODE>(pr, dout, lse2, delta, dq_acc, dq, dk, dv, dev, stream);
     };
-    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
+    return with_score_mode(pr.softcap, pr.slopes, run);
 }
 
 }  // namespace fa

@@ -91,10 +91,18 @@ __global__ void __launch_bounds__(128) bwd_delta_kernel(const __grid_constant__ 
                 mma_bf16_16816(dp, da, vf.x, vf.y);
                 mma_bf16_16816(dp, db, vf.z, vf.w);
             }
+            if constexpr ((MODE & kScoreCap) != 0) {
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 x = cap_pair_alone(make_float2(s[e], s[e + 1]), p.sc);
+                    s[e] = x.x;
+                    s[e + 1] = x.y;
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = e >> 1, key = kn + 2 * t + (e & 1);
-                float x = (MODE & kScoreCap) ? tanh_mufu(s[e] * p.sc.in) * p.sc.out_log2 : s[e] * p.scale_log2;
+                float x = s[e] * ((MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2);
                 if constexpr ((MODE & kScoreBias) != 0) x += bias_log2(static_cast<float>(row[r] + off - key), slope);
                 const bool keep = key >= key_lo[r] && key <= key_hi[r];
                 acc[r] += keep ? ex2_approx(x - l2[r]) * dp[e] : 0.f;
@@ -153,7 +161,7 @@ int launch_bwd_delta(const Problem& pr, const void* dout, const float* lse2, flo
     p.wr = pr.wr;
     p.sc = score_params(pr);
     auto run = [&](auto m) {
-        constexpr int MODE = decltype(m)::value;
+        constexpr int MODE = decltype(m)::value & ~kScoreWide;   // the kernel looks at the cap itself
         if constexpr (MODE != kScorePlain) {
             const unsigned grid = static_cast<unsigned>(blocks);
             switch (pr.D) {
@@ -165,7 +173,7 @@ int launch_bwd_delta(const Problem& pr, const void* dout, const float* lse2, flo
         }
         return cudaPeekAtLastError() == cudaSuccess ? 0 : 5;
     };
-    return with_score_mode(mode, run);
+    return with_score_mode(pr.softcap, pr.slopes, run);
 }
 
 }  // namespace fa

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(384, 1)
                     uint32_t sv[32];
                     tmem_ld32(tS + cc * 32, sv);
                     tmem_ld_wait_tie(sv);
-                    if constexpr ((MODE & kScoreCap) != 0) cap_scores(sv, p.sc, valid);
+                    if constexpr ((MODE & kScoreCap) != 0) cap_scores<(MODE & kScoreWide) != 0>(sv, p.sc, valid);
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -525,7 +525,7 @@ int launch_bwd_dq(const Problem& pr, const void* dout, const float* lse2, const 
             default: return 2;
         }
     };
-    return with_score_mode(score_mode(pr.softcap, pr.slopes), run);
+    return with_score_mode(pr.softcap, pr.slopes, run);
 }
 
 }  // namespace fa

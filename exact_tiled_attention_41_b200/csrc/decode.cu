@@ -114,7 +114,8 @@ template <int D>
 constexpr int dec_min_blocks() { return D == 256 ? 1 : 2; }
 
 // MODE: score modifiers (score.cuh).  A tile's 16 x 64 scores cost the multi-function unit at most three
-// results each (tanh and exponential), under a fifth of the time its keys and values take to arrive.
+// results each (tanh and exponential), under a fifth of the time its keys and values take to arrive; the tanh's
+// polynomial (caps beyond kNarrowCap) runs beside them on the FMA pipe.
 template <int D, int MODE>
 __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -269,10 +270,15 @@ __global__ void __launch_bounds__((kDecConsumers + 1) * 32, dec_min_blocks<D>())
         }
         // ---- cap and bias
         if constexpr ((MODE & kScoreCap) != 0) {
+            // element by element, not by a vote on the warp's range: rows past the sequence have no say
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[t][e] = tanh_mufu(sc[t][e] * p.sc.in);
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 x = cap_pair_alone(make_float2(sc[t][e], sc[t][e + 1]), p.sc);
+                    sc[t][e] = x.x;
+                    sc[t][e + 1] = x.y;
+                }
         }
         if constexpr ((MODE & kScoreBias) != 0) {
             const float mul = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;
@@ -746,7 +752,7 @@ static int run_decode(const KvCall& c, int chunk, void* workspace, const Device&
 
 int kvcache_launch(const KvCall& c, int chunk, void* workspace, const Device& dev, cudaStream_t stream) {
     auto run = [&](auto mode) {
-        constexpr int MODE = decltype(mode)::value;
+        constexpr int MODE = decltype(mode)::value & ~kScoreWide;   // the kernel looks at the cap itself
         switch (c.D) {
             case 64: return run_decode<64, MODE>(c, chunk, workspace, dev, stream);
             case 128: return run_decode<128, MODE>(c, chunk, workspace, dev, stream);
@@ -754,7 +760,7 @@ int kvcache_launch(const KvCall& c, int chunk, void* workspace, const Device& de
             default: return static_cast<int>(FA_ERR_UNSUPPORTED);
         }
     };
-    return with_score_mode(score_mode(c.softcap, c.slopes), run);
+    return with_score_mode(c.softcap, c.slopes, run);
 }
 
 }  // namespace fa

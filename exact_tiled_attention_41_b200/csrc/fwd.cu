@@ -217,9 +217,7 @@ __host__ __device__ constexpr int fma_exp_every(int D) {
 }
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// A cap beyond this needs a running maximum: 55 log2(e) < 80.
-constexpr float kMaxFixedCap = 55.f;
-constexpr int kScoreWide = 4;   // mode bit: a cap beyond kMaxFixedCap
+// A cap up to kNarrowCap needs no running maximum.
 __host__ __device__ constexpr bool fixed_reference(int mode) { return (mode & kScoreCap) && !(mode & kScoreWide); }
 
 // One tile of a row against its fixed reference: P = exp2(c2 tanh(in s) + bias - reference) for the BK scores at
@@ -286,7 +284,7 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
 // L2); otherwise each role walks the static boustrophedon deal itself (dense problems whose K and V fit
 // L2: the static deal is balanced there, and the feed's per-unit hand-off measured 2-3 % slower).
 // MODE: score modifiers (score.cuh).
-//  * Capped scores lie within +-cap, so unless the cap is beyond kMaxFixedCap no running maximum is needed: every row is
+//  * Capped scores lie within +-cap, so unless the cap is beyond kNarrowCap no running maximum is needed: every row is
 //    taken against a fixed reference, the largest bias among its allowed keys (0 without a bias) plus
 //    ScoreParams::ref_log2.  The scores above it are then at most 8 to 71 in log2 units, and the key with that bias lies at
 //    -88 or more: P, the sums and O stay inside fp32 and bf16 range, and the result is the same softmax (it
@@ -644,7 +642,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQ, BK, KST>::THREADS, 1)
                     for (int cc = 1; cc < BK / 32; ++cc) reg_tie(*reinterpret_cast<uint32_t(*)[32]>(sr + cc * 32));
                 }
                 float shift = 0.f;   // the row's part of the bias
-                if constexpr ((MODE & kScoreCap) != 0) cap_scores(s, p.sc, valid);
+                if constexpr ((MODE & kScoreCap) != 0) cap_scores<true>(s, p.sc, valid);
                 if constexpr ((MODE & kScoreBias) != 0)
                     shift = bias_scores(s, slope, static_cast<float>(at - kbase), p.wr == 0);
                 if (masked) {
@@ -867,11 +865,7 @@ static int run_fwd_d(const Problem& pr, void* out, float* lse, int* counter, con
             return local ? run_fwd<D, NQ, BK, KST, true, false, MODE>(pr, out, lse, nullptr, dev, stream)
                          : run_fwd<D, NQ, BK, KST, false, false, MODE>(pr, out, lse, nullptr, dev, stream);
     };
-    const int mode = score_mode(pr.softcap, pr.slopes);
-    if ((mode & kScoreCap) && pr.softcap > kMaxFixedCap)
-        return (mode & kScoreBias) ? run(std::integral_constant<int, kScoreCap | kScoreBias | kScoreWide>{})
-                                   : run(std::integral_constant<int, kScoreCap | kScoreWide>{});
-    return with_score_mode(mode, run);
+    return with_score_mode(pr.softcap, pr.slopes, run);
 }
 
 int launch_fwd(const Problem& pr, void* out, float* lse, int* counter, const Device& dev, cudaStream_t stream) {

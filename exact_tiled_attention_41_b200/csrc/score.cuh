@@ -18,6 +18,8 @@ namespace fa {
 
 // Score mode of a kernel instance, a bit mask; 0 leaves the kernels as they are without modifiers.
 constexpr int kScorePlain = 0, kScoreCap = 1, kScoreBias = 2;
+constexpr int kScoreWide = 4;          // a cap beyond kNarrowCap: another softmax reference and tanh
+constexpr float kNarrowCap = 55.f;     // 55 log2(e) < 80
 
 // Coefficients of the tanh polynomials, see cap_pair below.
 #define FA_TANH2 {0.12841614f, -0.33321908f, 0.9999996f}
@@ -62,14 +64,19 @@ inline ScoreParams score_params(const Problem& pr) {
     return score_params(pr.scale, pr.softcap, pr.slopes, pr.slope_sB);
 }
 
-// Calls run(std::integral_constant<int, mode>) for the mode asked for.
+// Calls run(std::integral_constant<int, mode>) for the modifiers given; the mode has kScoreWide where the cap asks for it.
 template <typename F>
-int with_score_mode(int mode, F&& run) {
-    switch (mode) {
+int with_score_mode(float softcap, const float* slopes, F&& run) {
+    const bool wide = softcap > kNarrowCap;
+    switch (score_mode(softcap, slopes)) {
         case kScorePlain: return run(std::integral_constant<int, kScorePlain>{});
-        case kScoreCap: return run(std::integral_constant<int, kScoreCap>{});
         case kScoreBias: return run(std::integral_constant<int, kScoreBias>{});
-        default: return run(std::integral_constant<int, kScoreCap | kScoreBias>{});
+        case kScoreCap:
+            return wide ? run(std::integral_constant<int, kScoreCap | kScoreWide>{})
+                        : run(std::integral_constant<int, kScoreCap>{});
+        default:
+            return wide ? run(std::integral_constant<int, kScoreCap | kScoreBias | kScoreWide>{})
+                        : run(std::integral_constant<int, kScoreCap | kScoreBias>{});
     }
 }
 
@@ -80,8 +87,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // tanh(x) = 1 - 2 / (1 + e^(2x)); absolute error about 2e-7 (ex2 and rcp on the multi-function unit are
-// good to 2 ulp; near 0 the difference cancels, so the error is relative to 1, not to x).  Large |x|
-// gives exactly +-1: e^(2x) becomes inf or 0.
+// good to 2 ulp; near 0 the difference cancels, so the error is relative to 1, not to x, and a score is off by 2e-7 of
+// the cap).  Large |x| gives exactly +-1: e^(2x) becomes inf or 0.
 __device__ __forceinline__ float tanh_mufu(float x) {
     const float e = ex2_approx(x * 2.885390081777927f);   // 2 log2(e)
     return fmaf(-2.f, rcp_approx(1.f + e), 1.f);
@@ -89,32 +96,57 @@ __device__ __forceinline__ float tanh_mufu(float x) {
 
 __device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
 
-// tanh(in * s) of a pair of raw scores, by the range of the arguments: x p(x^2) on the FMA pipe, with p of the
-// smallest maximum relative error on its range (exact_tiled_attention_41_b200/fit_tanh_poly.py prints the
-// coefficients; within 5e-7 relative for |x| <= 1/4, 2e-7 up to 1), or the multi-function unit.  A masked score, -inf,
-// stays -inf: the polynomials' leading coefficients are positive.
+// tanh(x) of a pair by the range of the arguments: x p(x^2) on the FMA pipe, with p of the smallest maximum relative
+// error on its range (exact_tiled_attention_41_b200/fit_tanh_poly.py prints the coefficients; within 5e-7 relative for
+// |x| <= 1/4, 2e-7 up to 1).  The polynomials' leading coefficients are positive: -inf stays -inf.
 static __constant__ float kTanh2[3] = FA_TANH2;
 static __constant__ float kTanh4[5] = FA_TANH4;
 static __constant__ float kTanh6[7] = FA_TANH6;
 enum TanhRange { kTanhQuarter, kTanhHalf, kTanhOne, kTanhAny };
 
 template <int RANGE>
+__device__ __forceinline__ float2 tanh_poly(float2 x) {
+    static_assert(RANGE != kTanhAny, "no polynomial reaches that far");
+    const float2 u = fmul2(x, x);
+    constexpr int DEG = RANGE == kTanhQuarter ? 2 : RANGE == kTanhHalf ? 4 : 6;
+    const float* c = RANGE == kTanhQuarter ? kTanh2 : RANGE == kTanhHalf ? kTanh4 : kTanh6;
+    float2 p = ffma2(splat2(c[0]), u, splat2(c[1]));
+#pragma unroll
+    for (int i = 2; i <= DEG; ++i) p = ffma2(p, u, splat2(c[i]));
+    return fmul2(p, x);
+}
+
+// tanh(x) of a pair, each within 3e-7 of its value whatever the other elements are: the polynomial up to 1, the
+// multi-function unit beyond, where its error relative to 1 is one relative to the value.  (The unit alone was off by 3 %
+// of the output at a cap of 1e6 and scores of a few units.)
+__device__ __forceinline__ float2 tanh_pair(float2 x) {
+    const float2 p = tanh_poly<kTanhOne>(x);
+    return make_float2(fabsf(x.x) <= 1.f ? p.x : tanh_mufu(x.x), fabsf(x.y) <= 1.f ? p.y : tanh_mufu(x.y));
+}
+
+// tanh(in * s) of a pair of raw scores, all of a warp's within RANGE.  Where some lie beyond 1 the unit serves all of them
+// for caps up to kNarrowCap, whose scores are then off by 1.1e-5 at most; WIDE, a larger cap, takes each by its size (in
+// the gradient kernels 4 to 8 % of the time at scores around the cap, and 3 % at small ones, which is why the narrow caps
+// do without).  A masked score, -inf, stays -inf.
+template <int RANGE, bool WIDE = false>
 __device__ __forceinline__ float2 cap_pair(float2 s, float2 in) {
     const float2 x = fmul2(s, in);
     if constexpr (RANGE == kTanhAny) {
-        return make_float2(s.x == -INFINITY ? -INFINITY : tanh_mufu(x.x), s.y == -INFINITY ? -INFINITY : tanh_mufu(x.y));
+        const float2 t = WIDE ? tanh_pair(x) : make_float2(tanh_mufu(x.x), tanh_mufu(x.y));
+        return make_float2(s.x == -INFINITY ? -INFINITY : t.x, s.y == -INFINITY ? -INFINITY : t.y);
     } else {
-        const float2 u = fmul2(x, x);
-        constexpr int DEG = RANGE == kTanhQuarter ? 2 : RANGE == kTanhHalf ? 4 : 6;
-        const float* c = RANGE == kTanhQuarter ? kTanh2 : RANGE == kTanhHalf ? kTanh4 : kTanh6;
-        float2 p = ffma2(splat2(c[0]), u, splat2(c[1]));
-#pragma unroll
-        for (int i = 2; i <= DEG; ++i) p = ffma2(p, u, splat2(c[i]));
-        return fmul2(p, x);
+        return tanh_poly<RANGE>(x);
     }
 }
 
-// out_log2 tanh(in s) + b of a pair of raw scores: the folded polynomials where they reach.
+// The same for a pair without a vote: the kernels whose tanh is little of their work.
+__device__ __forceinline__ float2 cap_pair_alone(float2 s, const ScoreParams& sc) {
+    const float2 x = fmul2(s, splat2(sc.in));
+    if (sc.out_log2 > kNarrowCap * 1.4426950408889634f) return tanh_pair(x);
+    return make_float2(tanh_mufu(x.x), tanh_mufu(x.y));
+}
+
+// out_log2 tanh(in s) + b of a pair of raw scores of a narrow cap: the folded polynomials where they reach.
 template <int RANGE>
 __device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc, float2 b) {
     if constexpr (RANGE == kTanhQuarter || RANGE == kTanhHalf) {
@@ -155,20 +187,20 @@ __device__ __forceinline__ float max_abs(const float (&s)[N]) {
 
 // s <- tanh(in * s) for a thread's block of raw scores; a thread that is not valid (a row past its sequence) has no
 // part in the warp's choice of polynomial
-template <int N>
+template <bool WIDE, int N>
 __device__ __forceinline__ void cap_scores(float (&s)[N], const ScoreParams& sc, bool valid = true) {
     with_tanh_range(valid ? max_abs(s) : 0.f, sc, [&](auto range) {
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-            const float2 t = cap_pair<decltype(range)::value>(make_float2(s[e], s[e + 1]), splat2(sc.in));
+            const float2 t = cap_pair<decltype(range)::value, WIDE>(make_float2(s[e], s[e + 1]), splat2(sc.in));
             s[e] = t.x;
             s[e + 1] = t.y;
         }
     });
 }
-template <int N>
+template <bool WIDE, int N>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreParams& sc, bool valid = true) {
-    cap_scores(reinterpret_cast<float (&)[N]>(s), sc, valid);
+    cap_scores<WIDE>(reinterpret_cast<float (&)[N]>(s), sc, valid);
 }
 
 // slope * log2(e) of query head h of sequence b

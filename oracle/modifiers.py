@@ -58,10 +58,15 @@ def head(q, k, v, scale, mask, softcap=0.0, slope=None, do=None, q_err=0.0):
     with np.errstate(divide="ignore"):
         lse = np.where(empty, 0.0, m)[:, 0] + np.log(l[:, 0])
     o = p @ v
-    # scores: D products summed in fp32 (each step off by 2^-23 of the running sum at most), the tanh by
-    # 4e-7 of the cap, the bias and its sum by 3 fp32 roundings; then one exponential, 2^-21 relative
+    # scores: D products summed in fp32 (each step off by 2^-23 of the running sum at most), the bias and its sum by
+    # 3 fp32 roundings; then one exponential, 2^-21 relative.  The tanh: its polynomials (arguments up to 1) are within
+    # 5e-7 of the value, and the multi-function unit's form, within 2e-7 of 1, is at most 2e-7 / tanh(1) = 2.7e-7 of it
+    # beyond: 6e-7 of the capped score with the rounding of the product.  Up to a cap of 55 the unit may serve smaller
+    # arguments too, off by 2e-7 of the cap (the bound takes twice that, as everywhere below it)
     size = scale * (np.abs(q) @ np.abs(k).T)
-    x_err = size * (q.shape[1] * 2.0 ** -23 + 2.0 ** -22 + q_err) + 4e-7 * softcap
+    x_err = size * (q.shape[1] * 2.0 ** -23 + 2.0 ** -22 + q_err)
+    if softcap > 0:
+        x_err = x_err + 4e-7 * np.minimum(softcap, np.maximum(1.5 * softcap * np.abs(t), 55.0))
     if slope is not None:
         i, j = np.arange(q.shape[0])[:, None], np.arange(k.shape[0])[None, :]
         x_err = x_err + 2.0 ** -22 * abs(slope) * np.abs(i + k.shape[0] - q.shape[0] - j)
