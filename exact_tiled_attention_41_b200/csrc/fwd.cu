@@ -240,6 +240,10 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
         tmem_ld_wait_tie(s[0]);
         reg_tie(s[1]);
         const float most = valid ? max_abs(x) : 0.f;
+        if (most == INFINITY) {   // a raw score beyond float32 is a score of -cap; -inf marks the masked ones below
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = x[c] == -INFINITY ? -3e38f : x[c];
+        }
         if (masked) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) x[c] = (c0 + c >= lo && c0 + c <= hi) ? x[c] : -INFINITY;

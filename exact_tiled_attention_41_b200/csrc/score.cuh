@@ -127,16 +127,13 @@ __device__ __forceinline__ float2 tanh_pair(float2 x) {
 // tanh(in * s) of a pair of raw scores, all of a warp's within RANGE.  Where some lie beyond 1 the unit serves all of them
 // for caps up to kNarrowCap, whose scores are then off by 1.1e-5 at most; WIDE, a larger cap, takes each by its size (in
 // the gradient kernels 4 to 8 % of the time at scores around the cap, and 3 % at small ones, which is why the narrow caps
-// do without).  A masked score, -inf, stays -inf.
+// do without).  A raw score beyond float32, +-inf, gives +-1: masks come later.
 template <int RANGE, bool WIDE = false>
 __device__ __forceinline__ float2 cap_pair(float2 s, float2 in) {
     const float2 x = fmul2(s, in);
-    if constexpr (RANGE == kTanhAny) {
-        const float2 t = WIDE ? tanh_pair(x) : make_float2(tanh_mufu(x.x), tanh_mufu(x.y));
-        return make_float2(s.x == -INFINITY ? -INFINITY : t.x, s.y == -INFINITY ? -INFINITY : t.y);
-    } else {
-        return tanh_poly<RANGE>(x);
-    }
+    if constexpr (RANGE != kTanhAny) return tanh_poly<RANGE>(x);
+    else if constexpr (WIDE) return tanh_pair(x);
+    else return make_float2(tanh_mufu(x.x), tanh_mufu(x.y));
 }
 
 // The same for a pair without a vote: the kernels whose tanh is little of their work.
@@ -146,7 +143,8 @@ __device__ __forceinline__ float2 cap_pair_alone(float2 s, const ScoreParams& sc
     return make_float2(tanh_mufu(x.x), tanh_mufu(x.y));
 }
 
-// out_log2 tanh(in s) + b of a pair of raw scores of a narrow cap: the folded polynomials where they reach.
+// out_log2 tanh(in s) + b of a pair of raw scores of a narrow cap: the folded polynomials where they reach.  A masked
+// score, -inf, stays -inf.
 template <int RANGE>
 __device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc, float2 b) {
     if constexpr (RANGE == kTanhQuarter || RANGE == kTanhHalf) {
@@ -161,7 +159,10 @@ __device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc,
         }
         return ffma2(s, p, b);
     } else {
-        return ffma2(cap_pair<RANGE>(s, splat2(sc.in)), splat2(sc.out_log2), b);
+        float2 t = cap_pair<RANGE>(s, splat2(sc.in));
+        if constexpr (RANGE == kTanhAny)
+            t = make_float2(s.x == -INFINITY ? -INFINITY : t.x, s.y == -INFINITY ? -INFINITY : t.y);
+        return ffma2(t, splat2(sc.out_log2), b);
     }
 }
 

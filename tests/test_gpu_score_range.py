@@ -1,8 +1,11 @@
 """Capped scores over the whole accepted range of caps and scores, on the GPU against the fp64 oracle."""
 
+import numpy as np
 import pytest
+import torch
 
-from exact_tiled_attention_41_b200 import workloads as W
+from exact_tiled_attention_41_b200 import abi, attention as A, workloads as W
+from tests.gpu_helpers import f64
 from tests.test_gpu_score_mod import NONE, check_cache, check_dense, slopes_of
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +43,41 @@ def test_rows_at_the_cap_beside_rows_far_below_it(D, softcap):
     c = W.kvcache_update(3, 4, 4, 2, D, 512, [5, 200, 508], seqlen_new=4, seed=D)
     c.tensors["q"][:, ::2] *= softcap
     check_cache(c, True, NONE, softcap, None)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap,slope", [(1.0, None), (1.0, 0.01), (60.0, None)])
+def test_raw_scores_beyond_float32(D, softcap, slope):
+    """q.k overflows to +-inf in float32: the tanh is +-1 there, in every path, and its derivative 0."""
+    S = 150
+    w = W.dense(1, S, S, 1, 1, D, True, seed=D)
+    t = w.tensors
+    sign = torch.ones(S)
+    sign[1::3] = -1
+    t["k"][0, :, 0] = 2e20 * sign[:, None].to(torch.bfloat16)
+    t["q"][0, :, 0] = 2e20 * ((-1.0) ** torch.arange(S))[:, None].to(torch.bfloat16)
+    slopes = None if slope is None else torch.tensor([slope])
+    sl = None if slope is None else slopes.cuda()
+    d = {n: x.cuda() for n, x in t.items()}
+    x = softcap * np.outer((-1.0) ** np.arange(S), sign.numpy())
+    if slope is not None:
+        x = x - slope * np.abs(np.arange(S)[:, None] - np.arange(S)[None, :])
+    x = np.where(np.tril(np.ones((S, S), bool)), x, -np.inf)
+    m = x.max(1, keepdims=True)
+    p = np.exp(x - m)
+    lse = m[:, 0] + np.log(p.sum(1))
+    p /= p.sum(1, keepdims=True)
+    o, v, do = p @ f64(t["v"])[0, :, 0], f64(t["v"])[0, :, 0], f64(t["do"])[0, :, 0]
+    # P rounded to bf16, the result rounded once more; the exponents are exact but for float32 roundings of the score
+    o_tol = 2.0 ** -7 * (p @ np.abs(v)) + 1e-6
+    lse_tol = 2.0 ** -20 * (1 + np.abs(lse))
+    out, l = A.flash_attn_func(d["q"], d["k"], d["v"], w.scale, True, NONE, softcap, sl)
+    assert (np.abs(f64(out)[0, :, 0] - o) <= o_tol).all() and (np.abs(f64(l)[0, 0] - lse) <= lse_tol).all()
+    for det in (False, True):
+        dq, dk, dv = A.flash_attn_backward(d["do"], d["q"], d["k"], d["v"], out, l, w.scale, True, NONE, det, softcap, sl)
+        assert (dq == 0).all() and (dk == 0).all()
+        assert (np.abs(f64(dv)[0, :, 0] - p.T @ do) <= 2.0 ** -7 * (p.T @ np.abs(do)) + 1e-6).all()
+    n = torch.tensor([S], dtype=torch.int32, device="cuda")
+    out, l = A.flash_attn_with_kvcache(d["q"], d["k"], d["v"], n, w.scale, True, softcap=softcap, alibi_slopes=sl)
+    assert (np.abs(f64(out)[0, :, 0] - o) <= o_tol).all() and (np.abs(f64(l)[0, 0] - lse) <= lse_tol).all()
+    assert abi.fa_get_device_status() == 0
