@@ -44,13 +44,15 @@ struct ScoreParams {
 inline ScoreParams score_params(float scale, float softcap, const float* slopes, int slope_sB) {
     ScoreParams sc = {softcap > 0.f ? scale / softcap : 0.f, softcap * 1.4426950408889634f, slopes, slope_sB};
     if (softcap > 0.f) {
-        // in^9 stays a normal float for in >= 2^-13; a smaller one (no usual scale and cap) does without the folded form
-        const bool fits = sc.in >= 0x1p-13f && sc.in <= 0x1p13f;
+        // the folded form serves while its coefficients (in^9 out_log2 the extreme one) are normal floats: one that became 0
+        // would make NaN of a masked score's infinite square.  No usual scale and cap goes beyond.
+        bool fits = sc.in >= 0x1p-13f && sc.in <= 0x1p13f;
         const double in = sc.in, c2[3] = FA_TANH2, c4[5] = FA_TANH4;
         double f = in * sc.out_log2;
         for (int k = 0; k < 5; ++k, f *= in * in) {
             if (k < 3) sc.fold2[2 - k] = make_float2(static_cast<float>(c2[2 - k] * f), static_cast<float>(c2[2 - k] * f));
             sc.fold4[4 - k] = make_float2(static_cast<float>(c4[4 - k] * f), static_cast<float>(c4[4 - k] * f));
+            fits = fits && fabs(c4[4 - k] * f) >= 0x1p-126 && fabs(c4[4 - k] * f) < 0x1p127;
         }
         sc.limit[0] = fits ? 0.25f / sc.in : -1.f;
         sc.limit[1] = fits ? 0.5f / sc.in : -1.f;

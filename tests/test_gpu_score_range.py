@@ -81,3 +81,14 @@ def test_raw_scores_beyond_float32(D, softcap, slope):
     out, l = A.flash_attn_with_kvcache(d["q"], d["k"], d["v"], n, w.scale, True, softcap=softcap, alibi_slopes=sl)
     assert (np.abs(f64(out)[0, :, 0] - o) <= o_tol).all() and (np.abs(f64(l)[0, 0] - lse) <= lse_tol).all()
     assert abi.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap,scale", [(1e-18, 1e-21), (1e-12, 2e-16), (1e-19, 1e-20)])
+@pytest.mark.parametrize("grow", [1, 4, 8, 13, 20, 60])
+def test_tiny_caps_and_scales_under_a_mask(D, softcap, scale, grow):
+    # the scores are nothing beside 1, whatever their ratio to the cap, so every allowed key weighs the same
+    w = W.dense(1, 200, 200, 2, 1, D, True, seed=grow)
+    w.scale = scale
+    w.tensors["q"].mul_(grow)
+    check_dense(w, (90, -1), softcap, None)
