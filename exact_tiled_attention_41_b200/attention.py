@@ -276,8 +276,9 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
     float32.  A token's position is its index in its sequence plus seqlen_offsets (an int, or int32 (B,)).
     Pairs are adjacent values (interleaved) or values rotary_dim / 2 apart.  inverse rotates by the opposite angle,
     which is the gradient (RotaryFunction records it for autograd; this call does not).  out may be x (in place);
-    other overlaps are not supported.  Returns out, contiguous unless given.  Rows behind the last sequence of a
-    packed batch are zeros in a new out and are not written in a given one.
+    other overlaps are not supported.  A given out is refused while gradients are recorded and it or x requires one,
+    and its version counter moves on, so that autograd notices where it had saved it.  Returns out, contiguous unless
+    given.  Rows behind the last sequence of a packed batch are zeros in a new out and are not written in a given one.
     """
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
@@ -310,10 +311,14 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have the shape and type of x")
+    elif torch.is_grad_enabled() and (x.requires_grad or out.requires_grad):
+        raise ValueError("x and a given out must not require grad: the rotation is not recorded (RotaryFunction records it)")
     if x.numel() == 0:
         return out
     _raise(abi.fa_rotary(x, out, cos, sin, cu_seqlens, offsets, seqlen_offsets, B, S, total, H, D, rd, rows,
                          *_rotary_strides(x, "x"), *_rotary_strides(out, "out"), interleaved, inverse, new), "fa_rotary")
+    if not new and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
     return out
 
 
