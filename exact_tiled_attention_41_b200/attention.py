@@ -177,13 +177,15 @@ def flash_attn_with_kvcache(q, k_cache, v_cache, cache_seqlens, softmax_scale=No
     With rotary_cos / rotary_sin (seqlen_ro, rotary_dim / 2) float32 (and k, v) the new keys are rotated at
     cache_seqlens, cache_seqlens + 1, ... on their way into the cache, and the queries at the same positions
     under a causal mask or window, else all at cache_seqlens; the pairs are adjacent values
-    (rotary_interleaved) or values rotary_dim / 2 apart.
+    (rotary_interleaved) or values rotary_dim / 2 apart.  Positions past the tables are refused for an int
+    cache_seqlens, and otherwise become zeros with an error in the device status (abi.fa_get_device_status).
     Returns (out (B, Sq, Hq, D), lse (B, Hq, Sq) or None).
     """
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _check(t, n)
     B, Sq, Hq, D = q.shape
-    if isinstance(cache_seqlens, int):
+    cached = cache_seqlens if isinstance(cache_seqlens, int) else None
+    if cached is not None:
         cache_seqlens = torch.full((B,), cache_seqlens, dtype=torch.int32, device=q.device)
     _check(cache_seqlens, "cache_seqlens", torch.int32)
     if (k is None) != (v is None):
@@ -209,6 +211,12 @@ def flash_attn_with_kvcache(q, k_cache, v_cache, cache_seqlens, softmax_scale=No
     nb = abi.fa_fwd_kvcache_mod_workspace_size(B, Hq, Hkv, Sq, D, cap, max_blocks, num_splits, rd)
     ws = _workspace(nb, q.device)
     left, right = _window(window_size)
+    if rd and cached is not None:
+        # the queries' last position, and that of the new keys which the cache has room for
+        room = cap * max(max_blocks, 1)
+        cached = min(max(cached, 0), room)
+        in_order = causal or 0 <= left < 1 << 30 or 0 <= right < 1 << 30
+        _check_positions(cached, max(cached + (Sq - 1 if in_order else 0), min(cached + sn, room) - 1), rows)
     _raise(abi.fa_fwd_kvcache_mod(q, k_cache, v_cache, cache_seqlens, k, v, sn, cache_batch_idx, block_table,
                                   max_blocks, cache_batch, cap, out, lse, B, Hq, Hkv, Sq, D, scale, causal, left,
                                   right, num_splits, *_score(softcap, alibi_slopes, q, B, Hq), rotary_cos, rotary_sin,
@@ -230,6 +238,12 @@ def _rotary_tables_shape(cos, sin, x, D):
     if half == 0 or 2 * half > D or half % 8 != 0:
         raise ValueError(f"rotary_dim must be a multiple of 16, at most {D}; got {2 * half}")
     return rows, 2 * half
+
+
+def _check_positions(first, last, rows):
+    """Refuses positions that the host knows: first (of 32 bits) and, where it is known, last (inside the tables)."""
+    if not -1 << 31 <= first < 1 << 31 or (last is not None and last >= rows):
+        raise ValueError(f"position {first if last is None else last} lies past the tables of {rows} rows")
 
 
 _SCALINGS = {"none": abi.FA_ROTARY_PLAIN, "linear": abi.FA_ROTARY_LINEAR, "base": abi.FA_ROTARY_BASE,
@@ -273,7 +287,9 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
 
     x (B, S, H, D), or (total, H, D) with cu_seqlens int32 (B + 1,): bf16 with the head dimension contiguous and
     the other strides multiples of 8 (a slice of a packed projection will do).  cos, sin (seqlen_ro, rotary_dim / 2)
-    float32.  A token's position is its index in its sequence plus seqlen_offsets (an int, or int32 (B,)).
+    float32.  A token's position is its index in its sequence plus seqlen_offsets (an int, or int32 (B,)).  Positions past
+    the tables are refused where they are known here (equal lengths and an int); else the call rotates to zeros there and
+    leaves an error in the device status (abi.fa_get_device_status).
     Pairs are adjacent values (interleaved) or values rotary_dim / 2 apart.  inverse rotates by the opposite angle,
     which is the gradient (RotaryFunction records it for autograd; this call does not).  out may be x (in place);
     other overlaps are not supported.  A given out is refused while gradients are recorded and it or x requires one,
@@ -315,6 +331,8 @@ def apply_rotary(x, cos, sin, seqlen_offsets=0, interleaved=True, inverse=False,
         raise ValueError("x and a given out must not require grad: the rotation is not recorded (RotaryFunction records it)")
     if x.numel() == 0:
         return out
+    if offsets is None:
+        _check_positions(seqlen_offsets, seqlen_offsets + S - 1 if cu_seqlens is None else None, rows)
     _raise(abi.fa_rotary(x, out, cos, sin, cu_seqlens, offsets, seqlen_offsets, B, S, total, H, D, rd, rows,
                          *_rotary_strides(x, "x"), *_rotary_strides(out, "out"), interleaved, inverse, new), "fa_rotary")
     if not new and not out.is_inference():

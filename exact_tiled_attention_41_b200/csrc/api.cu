@@ -595,6 +595,8 @@ int fa_rotary(const void* x, void* y, const float* rotary_cos, const float* rota
     if (rotary_dim <= 0 || rotary_dim > D || rotary_dim % 16 != 0) return FA_ERR_INVALID_ARG;
     if (rotary_len > kMaxSeqlen || S > kMaxSeqlen || seqlen_offset > kMaxSeqlen || num_seqs > kMaxSeqlen)
         return FA_ERR_UNSUPPORTED;
+    // a last position that is known here; the kernel looks at the others
+    if (cu_seqlens == nullptr && seqlen_offsets == nullptr && S > rotary_len - seqlen_offset) return FA_ERR_INVALID_ARG;
     RotaryCall c;
     c.tokens = cu_seqlens != nullptr ? total : static_cast<long long>(num_seqs) * S;
     const int st = check_tokens(c.tokens, H, D);

@@ -347,8 +347,10 @@ FA_API int fa_fwd_kvcache_mod(const void* q, void* k_cache, void* v_cache, const
  *         [num_seqs], or NULL: + seqlen_offset).
  *   rotary_cos, rotary_sin  float32 [rotary_len][rotary_dim / 2], 16-byte aligned;
  *         rotary_dim a multiple of 16, at most D.
- * A position outside the tables records FA_ERR_INVALID_ARG in the device status word, and
- * the rotated values of the row become zeros.  Rows of y outside every sequence of a packed
+ * A position outside the tables is refused (FA_ERR_INVALID_ARG) where the host knows it:
+ * without cu_seqlens and seqlen_offsets, S + seqlen_offset > rotary_len.  Otherwise it records
+ * FA_ERR_INVALID_ARG in the device status word, and the rotated values of the row become
+ * zeros.  Rows of y outside every sequence of a packed
  * batch (behind the last one) are left as they are, or with zero_tail != 0 (not in place)
  * become zeros, which is their gradient.  No workspace.
  */

@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from exact_tiled_attention_41_b200 import attention as A
+from exact_tiled_attention_41_b200 import abi, attention as A
 from tests.test_gpu_rotary import normal, tables
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +41,40 @@ def test_a_tensor_that_autograd_saved_may_not_change_under_it():
         z = normal(2, 2, 9, 3, 64).cuda()
         A.apply_rotary(z, cos.cuda(), sin.cuda(), out=z)
     assert torch.equal(z, x)
+
+
+def test_positions_that_the_host_knows_to_be_past_the_tables_are_refused():
+    x = normal(3, 2, 6, 2, 64).cuda()
+    cos, sin, _, _ = tables(10, 32)
+    cos, sin = cos.cuda(), sin.cuda()
+    A.apply_rotary(x, cos, sin, 4)
+    for offset in (5, 10, 1 << 20, 1 << 31, 1 << 32, (1 << 32) + 1):
+        with pytest.raises(ValueError, match="position"):
+            A.apply_rotary(x, cos, sin, offset)
+        with pytest.raises(ValueError, match="position"):
+            A.RotaryFunction.apply(x, cos, sin, offset)
+    cu = torch.tensor([0, 3, 6], dtype=torch.int32).cuda()
+    for offset in (1 << 31, 1 << 32):
+        with pytest.raises(ValueError, match="position"):
+            A.apply_rotary(x[0], cos, sin, offset, cu_seqlens=cu)
+    q, kc = normal(4, 2, 2, 2, 64).cuda(), normal(5, 2, 64, 2, 64).cuda()
+    before = kc.clone()
+    call = lambda n, **kw: A.flash_attn_with_kvcache(q, kc, kc.clone(), n, k=q, v=q, rotary_cos=cos, rotary_sin=sin, **kw)  # noqa: E731
+    for n in (9, 10, 63):
+        for kw in (dict(causal=True), dict()):
+            with pytest.raises(ValueError, match="position"):
+                call(n, **kw)
+    assert torch.equal(kc, before)
+    call(8)
+    call(8, causal=True)
+    assert abi.fa_get_device_status() == 0
+
+
+def test_a_full_cache_asks_for_no_position_of_keys_that_it_does_not_take():
+    # 64 rows, all in use: nothing is appended, and the query stands at position 64, the tables' last
+    cos, sin, _, _ = tables(65, 32)
+    q, kc = normal(6, 1, 1, 2, 64).cuda(), normal(7, 1, 64, 2, 64).cuda()
+    k = normal(8, 1, 3, 2, 64).cuda()
+    before = kc.clone()
+    A.flash_attn_with_kvcache(q, kc, kc.clone(), 64, k=k, v=k, rotary_cos=cos.cuda(), rotary_sin=sin.cuda())
+    assert torch.equal(kc, before) and abi.fa_get_device_status() == 0
