@@ -59,8 +59,10 @@ def _on_device(fn):
     """Runs fn with the device of its first tensor current (its stream and context are the ones used)."""
     @functools.wraps(fn)
     def run(*args, **kwargs):
-        t = args[0] if args else next(iter(kwargs.values()), None)
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        t = args[0] if args else None
+        if not isinstance(t, torch.Tensor):   # keywords in any order, a scale first perhaps
+            t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)), None)
+        if t is not None and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(t.device):
                 return fn(*args, **kwargs)
         return fn(*args, **kwargs)
