@@ -122,7 +122,7 @@ class FAError(RuntimeError):
 
 
 def _ptr(x):
-    return x if x is None or x.__class__ is int else x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 _current_stream = None

@@ -1,5 +1,6 @@
 """CPU checks of the host side of the calls: what the entry points do with their arguments before anything is launched."""
 
+import enum
 import os
 
 import pytest
@@ -64,3 +65,10 @@ def test_the_device_is_that_of_the_first_tensor_however_it_is_passed(monkeypatch
     assert run(None, q=t) == 4
     assert run(1, scale=2.0) == 4
     assert entered == ["cuda:1"] * 4
+
+
+def test_addresses_may_be_any_integers():
+    class Address(enum.IntEnum):
+        BUFFER = FAKE
+
+    assert abi._ptr(Address.BUFFER) == FAKE and abi._ptr(FAKE) == FAKE and abi._ptr(None) is None
