@@ -1256,7 +1256,7 @@ static int run_bwd(const Problem& pr, const void* out, const void* dout, const f
             pr.lse_sH, pr.lse_sT, l2_keep);
         if (cudaPeekAtLastError() != cudaSuccess) return 5;
     }
-    if (const int st = launch_bwd_delta(pr, dout, lse2, delta, stream)) return st;
+    if (const int st = launch_bwd_delta(pr, dout, lse2, delta, dev, stream)) return st;
 
     alignas(64) CUtensorMap mq, mk, mv, mdo;
     const uint64_t rq = static_cast<uint64_t>(pr.Hq) * D * 2, rk = static_cast<uint64_t>(pr.Hkv) * D * 2;
@@ -1346,7 +1346,7 @@ static int run_bwd_pp(const Problem& pr, const void* out, const void* dout, cons
             nullptr, nullptr, pr.Tq, pr.Hq, pr.Sq, pr.lse_sB, pr.lse_sH, pr.lse_sT, 0);
         if (cudaPeekAtLastError() != cudaSuccess) return 5;
     }
-    if (const int st = launch_bwd_delta(pr, dout, lse2, delta, stream)) return st;
+    if (const int st = launch_bwd_delta(pr, dout, lse2, delta, dev, stream)) return st;
     alignas(64) CUtensorMap mq, mk, mv, mdo;
     const uint64_t rq = static_cast<uint64_t>(pr.Hq) * D * 2, rk = static_cast<uint64_t>(pr.Hkv) * D * 2;
     if (!make_map_3d_bf16(&mq, pr.q, D, pr.Hq, pr.Tq, D * 2, rq, 64, 1, 64)) return 5;
@@ -1423,7 +1423,7 @@ static int run_bwd256(const Problem& pr, const void* out, const void* dout, cons
         det ? nullptr : dq_acc, bwd_unit_counter(workspace, pr.Tq, pr.Hq, D), pr.Tq, pr.Hq, pr.Sq, pr.lse_sB,
         pr.lse_sH, pr.lse_sT, 0);
     if (cudaPeekAtLastError() != cudaSuccess) return 5;
-    if (const int sd = launch_bwd_delta(pr, dout, lse2, delta, stream)) return sd;
+    if (const int sd = launch_bwd_delta(pr, dout, lse2, delta, dev, stream)) return sd;
     const int st = launch_bwd256_main(pr, dout, lse2, delta, dq_acc, dq, dk, dv, !det, dev, stream);
     if (st != 0 || !det) return st;
     return launch_bwd_dq(pr, dout, lse2, delta, dq, dev, stream);

@@ -84,8 +84,9 @@ int bwd_chunk_groups(int num_groups, int units_per_group, int group_q_heads, int
 // leaves dq alone (the deterministic backward computes it with launch_bwd_dq)
 int launch_bwd256_main(const Problem& pr, const void* dout, const float* lse2, const float* delta, float* dq_acc,
                        void* dq, void* dk, void* dv, bool with_dq, const Device& dev, cudaStream_t stream);
-// Delta from the probabilities (bwd_delta.cu) over the preprocess's, where score modifiers are used and it pays
-int launch_bwd_delta(const Problem& pr, const void* dout, const float* lse2, float* delta, cudaStream_t stream);
+// Delta from the probabilities (bwd_delta.cu) over the preprocess's, for rows of few keys where score modifiers are used
+int launch_bwd_delta(const Problem& pr, const void* dout, const float* lse2, float* delta, const Device& dev,
+                     cudaStream_t stream);
 // deterministic dQ: query-tile-stationary pass writing bf16 dq from LSE2 / Delta of the preprocess
 int launch_bwd_dq(const Problem& pr, const void* dout, const float* lse2, const float* delta, void* dq,
                   const Device& dev, cudaStream_t stream);

@@ -1,9 +1,12 @@
 """Capped scores over the whole accepted range of caps and scores, on the GPU against the fp64 oracle."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
+import oracle.modifiers as M
 from exact_tiled_attention_41_b200 import abi, attention as A, workloads as W
 from tests.gpu_helpers import f64
 from tests.test_gpu_score_mod import NONE, check_cache, check_dense, slopes_of
@@ -92,3 +95,58 @@ def test_tiny_caps_and_scales_under_a_mask(D, softcap, scale, grow):
     w.scale = scale
     w.tensors["q"].mul_(grow)
     check_dense(w, (90, -1), softcap, None)
+
+
+# ------------------------------------------------------------------------------------------- Delta
+def gradients(lens, Hq, Hkv, D, softcap, slopes, seed, det=True, only=None):
+    """Gradients (and the oracle's) of sequence `only` of a packed causal batch."""
+    w = W.varlen(lens, lens, Hq, Hkv, D, True, seed=seed)
+    w.tensors["q"].mul_(2)
+    t = {n: x.cuda() for n, x in w.tensors.items()}
+    sl = None if slopes is None else slopes.cuda()
+    where = (t["cu_q"], t["cu_k"], max(lens), max(lens))
+    out, lse = A.flash_attn_varlen_func(t["q"], t["k"], t["v"], *where, w.scale, True, NONE, softcap, sl)
+    g = A.flash_attn_varlen_backward(t["do"], t["q"], t["k"], t["v"], out, lse, *where, w.scale, True, NONE, det, softcap, sl)
+    cu = w.tensors["cu_q"].tolist()
+    a, b = cu[only], cu[only + 1]
+    cut = {n: w.tensors[n][a:b] for n in ("q", "k", "v", "do")}
+    ref = M.attention(*([f64(cut[n])] for n in ("q", "k", "v")), w.scale, True, NONE, softcap,
+                      None if slopes is None else slopes.numpy(), [f64(cut["do"])])[0]
+    return [x[a:b] for x in g], ref, cut
+
+
+def check_norms(g, ref):
+    # three roundings to bf16 at most, 1.6e-3 of the norm each on average (see test_gradients_of_rows_with_few_keys)
+    for name, x in zip(("dq", "dk", "dv"), g):
+        assert np.linalg.norm(f64(x) - ref[name]) <= 4e-3 * np.linalg.norm(ref[name]), name
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", [None, "falling"])
+@pytest.mark.parametrize("det", [False, True])
+def test_gradients_of_a_short_document_packed_beside_a_long_one(D, kind, det):
+    slopes = None if kind is None else slopes_of(4, kind=kind)
+    g, ref, _ = gradients([3000, 3, 2100], 4, 2, D, 20.0, slopes, D, det, 1)
+    check_norms(g, ref)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("steep", [4.0, 1.0, -2.0])
+def test_gradients_under_steep_slopes_in_a_long_sequence(D, softcap, steep):
+    # each row puts its weight on a few keys: the nearest, or the farthest
+    g, ref, _ = gradients([100, 1800, 2200], 4, 2, D, softcap, torch.tensor([steep] * 4), D + 1, True, 1)
+    check_norms(g, ref)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_gradients_of_a_sequence_do_not_depend_on_the_batch_around_it(D):
+    slopes = slopes_of(4, kind="mixed")
+    for n in (5, 60, 130):
+        long, _, cut = gradients([n, 2500, 2500], 4, 2, D, 8.0, slopes, n, True, 0)
+        t = {k: x.cuda()[None].contiguous() for k, x in cut.items()}
+        scale = 1.0 / math.sqrt(D)
+        out, lse = A.flash_attn_func(t["q"], t["k"], t["v"], scale, True, NONE, 8.0, slopes.cuda())
+        alone = A.flash_attn_backward(t["do"], t["q"], t["k"], t["v"], out, lse, scale, True, NONE, True, 8.0, slopes.cuda())
+        for x, y in zip(long, alone):
+            assert torch.equal(x, y[0])
