@@ -195,9 +195,10 @@ int launch_rotary(const RotaryCall& c, const Device& dev, cudaStream_t stream) {
 // The angle of row `pos` and pair i is pos * f_i.  An fp32 product would be off by pos * f * 2^-24 radians
 // (0.008 at position 131072), so the angle is formed in turns as an integer: turn_i = f_i / 2 pi as a 64-bit
 // fraction, and pos * turn_i modulo 2^64 is the fraction of a turn, off by at most pos * 2^-53 turns (f_i is
-// a double).  Its upper 32 bits give the nearest quarter turn and, as a signed number, what is left: an angle y
-// within pi / 4, exact to 2^-32 turns, whose sine and cosine are polynomials in y^2 (of the smallest maximum
-// relative error; exact_tiled_attention_41_b200/fit_trig_poly.py prints the coefficients).
+// a double): 1e-15 radians a position.  Its upper bits give the nearest quarter turn, and what is left, as a signed number
+// of all 64 bits, is an angle y within pi / 4 (slow pairs turn little at small positions, and their sines keep their
+// relative accuracy), whose sine and cosine are polynomials in y^2 (of the smallest maximum relative error;
+// exact_tiled_attention_41_b200/fit_trig_poly.py prints the coefficients).
 struct TableParams {
     uint64_t turn[128];   // rd / 2 <= 128 pairs
     float* cos;
@@ -206,10 +207,11 @@ struct TableParams {
     float amplitude;
 };
 
-// sine and cosine of a fraction of a turn
-__device__ __forceinline__ void sin_cos_turn(uint32_t frac, float& sn, float& cs) {
-    const uint32_t quarter = (frac + 0x20000000u) >> 30;
-    const float y = static_cast<float>(static_cast<int32_t>(frac - (quarter << 30))) * 1.4629180792671596e-9f;   // 2 pi 2^-32
+// sine and cosine of a fraction of a turn, in units of 2^-64
+__device__ __forceinline__ void sin_cos_turn(uint64_t frac, float& sn, float& cs) {
+    const uint32_t quarter = (static_cast<uint32_t>(frac >> 32) + 0x20000000u) >> 30;
+    const int64_t left = static_cast<int64_t>(frac - (static_cast<uint64_t>(quarter) << 62));
+    const float y = static_cast<float>(left) * 3.4061215800865545e-19f;   // 2 pi 2^-64
     const float u = y * y;
     float s = fmaf(-0.00019501822f, u, 0.00833201688f);
     s = fmaf(s, u, -0.166666508f);
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant
         float s[4], c[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            sin_cos_turn(static_cast<uint32_t>(frac[e] >> 32), s[e], c[e]);
+            sin_cos_turn(frac[e], s[e], c[e]);
             frac[e] += step[e];
         }
         const float a = p.amplitude;

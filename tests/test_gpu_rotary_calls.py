@@ -1,9 +1,12 @@
-"""Calls of the rotary entry points that must not pass silently."""
+"""Calls of the rotary entry points that must not pass silently, and the relative accuracy of small sines."""
 
+import numpy as np
 import pytest
 import torch
 
+import oracle.modifiers as M
 from exact_tiled_attention_41_b200 import abi, attention as A
+from tests.gpu_helpers import f64
 from tests.test_gpu_rotary import normal, tables
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +81,19 @@ def test_a_full_cache_asks_for_no_position_of_keys_that_it_does_not_take():
     before = kc.clone()
     A.flash_attn_with_kvcache(q, kc, kc.clone(), 64, k=k, v=k, rotary_cos=cos.cuda(), rotary_sin=sin.cuda())
     assert torch.equal(kc, before) and abi.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 32.0), ("base", 16.0), ("by_parts", 32.0)])
+def test_small_sines_are_as_accurate_as_large_ones(scaling, factor):
+    rows, rd, base = 300, 128, 1e6
+    cos, sin = A.rotary_tables(rows, rd, base, scaling, factor, original_seqlen=4096)
+    c, s = M.rotary_tables(rows, rd, base, scaling, factor, original=4096)
+    # The turn of a position is kept to 2^-63 (and 2^-53 of itself): an angle off by pos 2 pi 2^-63.  Then float32: the
+    # angle's conversion and product, its square, and the polynomial with its last product, 4 half steps relative; a
+    # quarter turn on, the cosine's polynomial, 2 half steps of 1.  Where the angle comes back near a multiple of a quarter
+    # turn, the bound on the angle in turns counts, not its relative size.
+    pos = np.arange(rows)[:, None]
+    angle = pos * (2 * np.pi * 2.0 ** -63) + 2.0 ** -50 * pos
+    for got, want in ((cos, c), (sin, s)):
+        err = np.abs(f64(got) - want)
+        assert (err <= 5 * 2.0 ** -24 * np.abs(want) + angle).all()
