@@ -240,13 +240,9 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
         tmem_ld_wait_tie(s[0]);
         reg_tie(s[1]);
         const float most = valid ? max_abs(x) : 0.f;
-        if (most == INFINITY) {   // a raw score beyond float32 is a score of -cap; -inf marks the masked ones below
+        if (masked) {   // -inf marks the masked ones; a raw score beyond float32 is a score of -cap
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = x[c] == -INFINITY ? -3e38f : x[c];
-        }
-        if (masked) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = (c0 + c >= lo && c0 + c <= hi) ? x[c] : -INFINITY;
+            for (int c = 0; c < 64; ++c) x[c] = (c0 + c >= lo && c0 + c <= hi) ? max_nan(x[c], -3e38f) : -INFINITY;
         }
         // the bias less the reference: linear in the column on either side of the diagonal, step c + base
         const int dc = d0 - c0;
@@ -264,7 +260,7 @@ __device__ __forceinline__ float softmax_fixed(uint32_t tS, const ScoreParams& s
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const float2 b = (MODE & kScoreBias) ? make_float2(bias(2 * e), bias(2 * e + 1)) : splat2(-sc.ref_log2);
-                const float2 y = cap_pair_log2<decltype(range)::value>(make_float2(x[2 * e], x[2 * e + 1]), sc, b);
+                const float2 y = cap_pair_log2<decltype(range)::value>(make_float2(x[2 * e], x[2 * e + 1]), sc, b, masked);
                 const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                 if (e & 1) sum1 = fadd2(sum1, pr); else sum0 = fadd2(sum0, pr);
                 pk[e] = pack_bf16x2(pr.x, pr.y);

@@ -145,10 +145,17 @@ __device__ __forceinline__ float2 cap_pair_alone(float2 s, const ScoreParams& sc
     return make_float2(tanh_mufu(x.x), tanh_mufu(x.y));
 }
 
-// out_log2 tanh(in s) + b of a pair of raw scores of a narrow cap: the folded polynomials where they reach.  A masked
-// score, -inf, stays -inf.
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// out_log2 tanh(in s) + b of a pair of raw scores of a narrow cap: the folded polynomials where they reach.  Where some
+// scores of the tile are masked, -inf is their mark and stays -inf.
 template <int RANGE>
-__device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc, float2 b) {
+__device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc, float2 b, bool masked) {
     if constexpr (RANGE == kTanhQuarter || RANGE == kTanhHalf) {
         const float2 w = fmul2(s, s);
         float2 p;
@@ -163,7 +170,7 @@ __device__ __forceinline__ float2 cap_pair_log2(float2 s, const ScoreParams& sc,
     } else {
         float2 t = cap_pair<RANGE>(s, splat2(sc.in));
         if constexpr (RANGE == kTanhAny)
-            t = make_float2(s.x == -INFINITY ? -INFINITY : t.x, s.y == -INFINITY ? -INFINITY : t.y);
+            t = make_float2(masked && s.x == -INFINITY ? -INFINITY : t.x, masked && s.y == -INFINITY ? -INFINITY : t.y);
         return ffma2(t, splat2(sc.out_log2), b);
     }
 }
