@@ -339,12 +339,6 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
     return d;
 }
 
-__device__ __forceinline__ float min3f(float a, float b, float c) {
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // Packed two-lane fp32 arithmetic (PTX fma/add/mul .f32x2, round to nearest even).
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
     uint64_t d, x, y, z;
