@@ -17,7 +17,7 @@
 // 4 in all heads 1.1e-2, 162 us and 2.3e-3, 198 us; 0.5: 4.2e-3 and 2.3e-3; a slope of 0.25, left as it is, 3.7e-3.  The
 // look at the blocks alone, where no head is steep, costs 5 us.
 //
-// A warp takes 16 query rows of a head and their keys 16 at a time: 16 x 16 scores and dP with bf16 mma.sync (16 rows could
+// A warp takes 16 query rows of a head and their keys 8 at a time: 16 x 8 scores and dP with bf16 mma.sync (16 rows could
 // not fill a 128-row tcgen05 tile, and the work is small by the rule).  Bound by the latency of its loads, so many warps
 // are wanted: with four warps to a block of rows, each with every fourth tile of 16 keys, windows of 2 to 16 keys took 32 us
 // of the backward above, and take 22 to 24 so.  A warp looks at 32 blocks of rows at once for those that are to be summed.
@@ -189,7 +189,7 @@ int launch_bwd_delta(const Problem& pr, const void* dout, const float* lse2, flo
     p.blocks = (pr.Sq + 15) / 16;
     if (pr.cu_q == nullptr && !(mode & kScoreBias) && !delta_whole(pr.Sq, pr.Sk, pr.wl, pr.wr)) return 0;
     const long long units = static_cast<long long>(p.blocks) * pr.Hq * pr.num_seqs;
-    if (units > 0x7fffffffLL) return 0;
+    if (units > 0x7fffffffLL) return 0;   // some 10^10 rows
     p.units = static_cast<int>(units);
     p.q = static_cast<const __nv_bfloat16*>(pr.q);
     p.k = static_cast<const __nv_bfloat16*>(pr.k);

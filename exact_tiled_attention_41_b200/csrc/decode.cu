@@ -633,9 +633,11 @@ int kvcache_chunk(const KvCall& c, int num_sms) {
     } else if (score_mode(c.softcap, c.slopes) != kScorePlain) {
         // about 2.5 waves of resident split CTAs, assuming caches half full on average (the whole call, B200: 32 x 8
         // heads of 1-8K keys, D = 128: 14 splits, 6 waves, 124 us, 5 splits 119.5; 16 x 16 heads of 512-2052 keys,
-        // D = 256, one CTA per SM: 5 splits 85 us, 3 splits 77).  At least 512 keys a split, or 256 where 512 would
-        // leave SMs idle (one sequence of 1235 keys, 4 heads: 14.5 us with 512, 12.1 with 256).  Calls without
-        // modifiers keep the split, and the bits, that they had.
+        // D = 256, one CTA per SM: 5 splits 85 us, 3 splits 77).  On long caches the choice matters little (64 x 8 heads of
+        // 1-16K keys, D = 128: 3 splits, this rule's, 329 us, 6 splits 331, 7 splits, the other rule's, 343; 4 new tokens 352,
+        // 357, 366).  At least 512 keys a split, or 256 where 512 would leave SMs idle (one sequence of 1235 keys, 4 heads:
+        // 14.5 us with 512, 12.1 with 256).  Modifiers do not ask for another split: calls without them keep the one, and
+        // the bits, that they had.
         const long long resident = static_cast<long long>(num_sms) * (c.D == 256 ? 1 : 2);
         ch = parallel * cap / (5 * resident);
         const long long least = parallel * ((cap + 511) / 512) < resident ? 256 : 512;

@@ -128,8 +128,8 @@ __device__ __forceinline__ float2 tanh_pair(float2 x) {
 
 // tanh(in * s) of a pair of raw scores, all of a warp's within RANGE.  Where some lie beyond 1 the unit serves all of them
 // for caps up to kNarrowCap, whose scores are then off by 1.1e-5 at most; WIDE, a larger cap, takes each by its size (in
-// the gradient kernels 4 to 8 % of the time at scores around the cap, and 3 % at small ones, which is why the narrow caps
-// do without).  A raw score beyond float32, +-inf, gives +-1: masks come later.
+// the gradient kernels 9 % of the time at scores around the cap, and 3 % at small ones, which is why the narrow caps do
+// without).  A raw score beyond float32, +-inf, gives +-1: masks come later.
 template <int RANGE, bool WIDE = false>
 __device__ __forceinline__ float2 cap_pair(float2 s, float2 in) {
     const float2 x = fmul2(s, in);

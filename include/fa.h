@@ -261,7 +261,11 @@ FA_API int fa_fwd_kvcache_ex(const void* q, void* k_cache, void* v_cache, const 
  * formula, and the tanh above is the reading taken.)  The *_ex calls are these with
  * softcap = 0 and alibi_slopes = NULL, and give the same bits.
  *   softcap       0 = no cap; else positive and finite, at most 1e20, with
- *                 1e-20 <= softmax_scale / softcap <= 1e20.
+ *                 1e-20 <= softmax_scale / softcap <= 1e20.  q . k beyond float32 counts as
+ *                 +-softcap.  Up to 55 the softmax is taken against a fixed reference, with
+ *                 probabilities between 2^-88 and 2^71 before they are divided by their sum: the
+ *                 largest |v| times the number of keys must stay below 1e17, and values of v below
+ *                 1e-11 may be lost in rows whose scores all lie near -softcap.
  *   alibi_slopes  DEVICE float32, slope of query head h of sequence b at
  *                 alibi_slopes[b * alibi_batch_stride + h], of either sign, magnitude
  *                 at most 1e10; NULL = no bias.  alibi_batch_stride is 0 (one set of
