@@ -8,14 +8,16 @@
 // Only calls with score modifiers use it (the others keep the bits they had), and of their rows those that see few keys;
 // for the others the preprocess's sum stands.  The choice follows from a row's own sequence, mask and slope, so the
 // gradients of a sequence do not depend on the batch that it stands in:
-//  * a window of at most 16 keys, a sequence of at most 64 keys, or of at most 16 queries (and 1024 keys): all of a
-//    row's keys;
+//  * its rows see at most 16 keys (of a window, or of the sequence); at most 64 where the sequence has at most 512 queries, or
+//    1024 where it has at most 16, since a gradient of few rows averages less: all of a row's keys;
 //  * a head with a steep slope: the 48 keys with the largest bias, for the rows that put all but 2^-12 of their weight
 //    there (what is left out is then below the rounding that this replaces).
 // Error of dq (relative Frobenius norm) and time of the whole backward, without and with it (B200, 2 x 2048 causal tokens,
-// 16 heads of 128, cap 30): windows of 17 keys 3.4e-3, 72 us and 2.4e-3, some 95 us, so wider windows do without; slopes of
+// 16 heads of 128, cap 30): windows of 17 keys 3.4e-3, 72 us and 2.4e-3, some 95 us, so they do without; slopes of
 // 4 in all heads 1.1e-2, 162 us and 2.3e-3, 198 us; 0.5: 4.2e-3 and 2.3e-3; a slope of 0.25, left as it is, 3.7e-3.  The
-// look at the blocks alone, where no head is steep, costs 5 us.
+// look at the blocks alone, where no head is steep, costs 5 us.  Short sequences pay most, for Q, K, V and dO are read once
+// more: 512 packed ones of 64 tokens 578 us without, 749 with it (dq off by 3.0e-3 and 2.4e-3); 150 queries on 97 keys
+// through a window of 41, cap and bias: 3.7e-3 and 2.4e-3 in some 4 us.
 //
 // A warp takes 16 query rows of a head and their keys 8 at a time: 16 x 8 scores and dP with bf16 mma.sync (16 rows could
 // not fill a 128-row tcgen05 tile, and the work is small by the rule).  Bound by the latency of its loads, so many warps
@@ -36,7 +38,8 @@ constexpr float kDeltaSteep = 0.5f;   // natural units: exp(-0.5 * 17) < 2^-12
 
 // The rows of a sequence see few keys whatever the slope.
 __host__ __device__ constexpr bool delta_whole(int Lq, int Lk, int wl, int wr) {
-    return (wl >= 0 && wr >= 0 && wl < 16 && wl + wr < 16) || Lk <= 64 || (Lq <= 16 && Lk <= 1024);
+    const int keys = wl >= 0 && wr >= 0 && wl < Lk && wr < Lk - wl ? wl + wr + 1 : Lk;   // that a row can see
+    return keys <= 16 || (Lq <= 512 && keys <= 64) || (Lq <= 16 && keys <= 1024);
 }
 
 struct DeltaParams {
