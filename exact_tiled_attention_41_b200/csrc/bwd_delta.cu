@@ -8,8 +8,8 @@
 // Only calls with score modifiers use it (the others keep the bits they had), and of their rows those that see few keys;
 // for the others the preprocess's sum stands.  The choice follows from a row's own sequence, mask and slope, so the
 // gradients of a sequence do not depend on the batch that it stands in:
-//  * its rows see at most 16 keys (of a window, or of the sequence); at most 64 where the sequence has at most 512 queries, or
-//    1024 where it has at most 16, since a gradient of few rows averages less: all of a row's keys;
+//  * its rows see at most 16 keys (of a window, or of the sequence), or at most 64 where the sequence has at most 512
+//    queries, since a gradient of few rows averages less: all of a row's keys;
 //  * a head with a steep slope: the 48 keys with the largest bias, for the rows that put all but 2^-12 of their weight
 //    there (what is left out is then below the rounding that this replaces).
 // Error of dq (relative Frobenius norm) and time of the whole backward, without and with it (B200, 2 x 2048 causal tokens,
@@ -39,7 +39,7 @@ constexpr float kDeltaSteep = 0.5f;   // natural units: exp(-0.5 * 17) < 2^-12
 // The rows of a sequence see few keys whatever the slope.
 __host__ __device__ constexpr bool delta_whole(int Lq, int Lk, int wl, int wr) {
     const int keys = wl >= 0 && wr >= 0 && wl < Lk && wr < Lk - wl ? wl + wr + 1 : Lk;   // that a row can see
-    return keys <= 16 || (Lq <= 512 && keys <= 64) || (Lq <= 16 && keys <= 1024);
+    return keys <= 16 || (Lq <= 512 && keys <= 64);
 }
 
 struct DeltaParams {
