@@ -156,7 +156,8 @@ struct BwdCfg {
     static constexpr uint32_t OFF_K = 0, OFF_V = T_BYTES, OFF_Q = 2 * T_BYTES, OFF_DO = (2 + ST) * T_BYTES,
                               OFF_DS = (2 + 2 * ST) * T_BYTES, OFF_STAT = OFF_DS + DS_BYTES,
                               OFF_BAR = OFF_STAT + 2 * ST * 128 * 4;
-    static constexpr int NUM_BARS = 2 + 2 * ST + 10 + 2 * kFeedSlots;
+    static constexpr int BAR_JOIN = 2 + 2 * ST + 10 + 2 * kFeedSlots;   // a compute warpgroup's own, one each
+    static constexpr int NUM_BARS = BAR_JOIN + 2;
     static constexpr size_t SMEM = OFF_BAR + NUM_BARS * 8 + 16 + 4 * kFeedSlots;
     // tensor memory: dV | dK | S^T | dP^T.  After the gradient step the packed bf16 P^T and dS^T of each
     // 32-query half sit in that half's own 32 columns of S^T; dQ (fp32, D columns) is accumulated over
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(bars + 2 + 2 * ST + 10 + s, 1);                            // unit published
             mbar_init(bars + 2 + 2 * ST + 10 + kFeedSlots + s, DQ ? 14 : 10);    // read by the issuers, compute (, dQ) warps
         }
+        for (int s = 0; s < 2; ++s) mbar_init(bars + C::BAR_JOIN + s, 4);        // the four warps of a compute warpgroup
         mbar_init(bars + C::NUM_BARS + 1, 1);   // raw: a tile that ends past its sequence has arrived
         *abort_flag = 0;
         fence_mbar_init();
@@ -478,8 +480,15 @@ __global__ void __launch_bounds__(512, 1)
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lb = tmem_lane_base(warp & 3);
         const float c2 = (MODE & kScoreCap) ? p.sc.out_log2 : p.scale_log2;   // score (tanh) -> log2 units
-        uint32_t unit_it = 0, q_it = 0, g_it = 0;
+        uint32_t unit_it = 0, q_it = 0, g_it = 0, join_it = 0;
         bool ok = true;
+        // the warpgroup's warps meet; a wait like the others, with a limit, for a warp that has given up does not come
+        auto join = [&]() -> bool {
+            const uint32_t bar = b0 + 8u * (C::BAR_JOIN + gq);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            return mbar_wait_warp(bar, join_it++ & 1, w);
+        };
         for (uint32_t fi = 0; ok; ++fi) {
             int u;
             if (!feed_get(feed, fi, u, w, true)) { ok = false; break; }
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(512, 1)
                 for (int bx = 0; bx < D / 64; ++bx) {
                     if (bx > 0) {
                         if (issuer) bulk_wait_read_all();
-                        named_bar_sync(1 + gq, 128);
+                        if (!join()) { ok = false; break; }
                     }
 #pragma unroll 1
                     for (int cc = 0; cc < 2; ++cc) {
@@ -636,7 +645,7 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     fence_proxy_async_smem();
-                    named_bar_sync(1 + gq, 128);
+                    if (!join()) { ok = false; break; }
                     if (issuer) {
                         tma_store_3d(map, smem_u32(half_buf), bx * 64, te.hk, te.k_start + te.n0);
                         bulk_commit();
@@ -644,7 +653,7 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 // the next tile's dS^T rows go into this buffer: wait until the last store has read it
                 if (issuer) bulk_wait_read_all();
-                named_bar_sync(1 + gq, 128);
+                if (!ok || !join()) { ok = false; break; }
             } else {
                 // the sequence's last, partial key tile: rows leave through 2 KB per warp of the same
                 // buffer, 8 rows x 64 bytes per store, and only the rows inside the sequence are written

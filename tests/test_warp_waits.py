@@ -54,3 +54,11 @@ def test_the_unit_feed_votes_for_whole_warps():
     assert "whole_warp ? mbar_wait_warp(" in body[:body.index("\n}\n")]
     body = src[src.index("bool mbar_wait_warp("):]
     assert "__all_sync(0xffffffffu, mbar_wait(bar, parity, w))" in body[:body.index("\n}\n")]
+
+
+@pytest.mark.parametrize("name", ["fwd.cu", "bwd.cu", "bwd256.cu", "bwd_dq.cu", "sm100.cuh"])
+def test_no_wait_without_a_limit_between_warps_that_may_give_up(name):
+    # a warp that has given up does not come to a hardware barrier, and the others would stay there for good; the barriers
+    # of the whole block (__syncthreads) stand where every role arrives, whatever became of it
+    src = open(os.path.join(CSRC, name)).read()
+    assert not re.search(r"bar\.sync|barrier\.sync|named_bar", re.sub(r"//[^\n]*", "", src))
